@@ -21,6 +21,7 @@ QLIN_F32, QLIN_BF16 = 0, 1
 QLIN_EPI_NONE, QLIN_EPI_SILU_GATE, QLIN_OUT_BF16, QLIN_FLAG_PDL, QLIN_FLAG_CTA_PAIRS = 0, 1, 0x10, 0x100, 0x200
 QLIN_FLAG_BF16_COPY = 0x400
 QLIN_PACK_DEFAULT, QLIN_PACK_GATE_UP, QLIN_PACK_MMA, QLIN_PACK_MMA_BF16 = 0, 1, 2, 4
+QLIN_ROPE_HALVES, QLIN_ROPE_INTERLEAVED = 0, 1
 QLIN_OP_GEMV, QLIN_OP_MOE, QLIN_OP_CHUNK, QLIN_OP_MOE_PREFILL = 1, 2, 3, 4
 STATUS = {0: "QLIN_OK", 1: "QLIN_ERR_INVALID_ARG", 2: "QLIN_ERR_UNSUPPORTED",
           3: "QLIN_ERR_ALIGNMENT", 4: "QLIN_ERR_WORKSPACE", 5: "QLIN_ERR_CUDA",
@@ -49,6 +50,12 @@ SIGNATURES = {
     "qlin_chain_max_ops": (_I, []),
     "qlin_chain_workspace_bytes": (_SZ, [_I, _I, _P, _I]),
     "qlin_gemv_chain": (_I, [_I, _I, _I, _P, _I, _I, _P, _SZ, _P]),
+    "qlin_kv_cache_bytes": (_SZ, [_I64, _I, _I, _I]),
+    "qlin_qk_norm_rope": (_I, [_P, _I, _I64, _I64, _I, _I, _I, _P, _P, _P, _I64, _P, _I64, _I, _I, _P, _SZ, _P]),
+    "qlin_kv_append": (_I, [_P, _P, _I, _I64, _I64, _I, _P, _P, _P, _P, _I64, _I, _P, _SZ, _P]),
+    "qlin_kv_gather": (_I, [_P, _I64, _P, _P, _P, _I, _P, _SZ, _P]),
+    "qlin_attn_kv4_workspace_bytes": (_SZ, [_P, _I, _I, _I]),
+    "qlin_attn_kv4": (_I, [_P, _P, _I64, _P, _I64, _I, _P, _P, _I, _I, _I64, _I, _F, _I, _P, _I64, _I, _P, _SZ, _P]),
     "qlin_ws_status": (_I, [_P, _P]),
     "qlin_ws_set_wait_budget": (_I, [_P, ctypes.c_uint32, _P]),
     "qlin_probe_fp4_mma": (_I, [_I, _P, _I, _P, ctypes.POINTER(_I), _P]),
@@ -60,6 +67,18 @@ class GemvOp(ctypes.Structure):
     """struct qlin_gemv_op of include/qlin.h (64 bytes)."""
     _fields_ = [("packed", _P), ("N", _I64), ("K", _I64), ("x", _P), ("ldx", _I64), ("y", _P),
                 ("ldy", _I64), ("epilogue", ctypes.c_int32), ("wait_for", ctypes.c_int32)]
+
+
+class KVCacheDesc(ctypes.Structure):
+    """struct qlin_kv_cache of include/qlin.h (40 bytes)."""
+    _fields_ = [("data", _P), ("n_pages", _I64), ("page", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("k_scale", _F), ("v_scale", _F)]
+
+
+class QKParams(ctypes.Structure):
+    """struct qlin_qk_params of include/qlin.h (48 bytes)."""
+    _fields_ = [("q_weight", _P), ("k_weight", _P), ("cos_sin", _P), ("n_pos", _I64), ("rot", ctypes.c_int32),
+                ("flags", ctypes.c_int32), ("eps", _F)]
 
 
 class QlinError(RuntimeError):
@@ -347,3 +366,190 @@ def qlin_gemv_chain(fmt, xdt, M, ops, flags=0, ws=None, stream=None):
                                ws.numel() * ws.element_size(), _stream(stream))
     _check("qlin_gemv_chain", st)
     return ws
+
+
+# ----------------------------------------------------------------------------- queries, keys and the 4-bit cache
+_XDT = {torch.float32: QLIN_F32, torch.bfloat16: QLIN_BF16}
+_YDT = {QLIN_F32: torch.float32, QLIN_BF16: torch.bfloat16}
+
+
+def qlin_kv_cache_bytes(n_pages, page, Hkv, D):
+    return lib().qlin_kv_cache_bytes(n_pages, page, Hkv, D)
+
+
+class KVCache:
+    """A paged NVFP4 cache of keys and values over the uint8 CUDA tensor `data` (a contiguous buffer of whole
+    pages, 256-byte aligned; kv_cache(...) allocates one)."""
+
+    def __init__(self, data, page, Hkv, D, k_scale=1.0, v_scale=1.0):
+        per = qlin_kv_cache_bytes(1, page, Hkv, D)
+        if per == 0:
+            raise QlinError("qlin_kv_cache_bytes", 1)
+        if not isinstance(data, torch.Tensor) or not data.is_cuda or data.dtype != torch.uint8 or not data.is_contiguous():
+            raise TypeError("data must be a contiguous uint8 CUDA tensor")
+        if data.numel() == 0 or data.numel() % per:
+            raise ValueError(f"data must hold whole pages of {per} bytes")
+        self.data, self.page, self.Hkv, self.D = data, page, Hkv, D
+        self.n_pages = data.numel() // per
+        self.desc = KVCacheDesc(data.data_ptr(), self.n_pages, page, Hkv, D, k_scale, v_scale)
+        self.ref = ctypes.addressof(self.desc)
+
+
+def kv_cache(n_pages, page, Hkv, D, k_scale=1.0, v_scale=1.0, device="cuda"):
+    """A zero-filled cache of n_pages pages."""
+    nbytes = qlin_kv_cache_bytes(n_pages, page, Hkv, D)
+    if nbytes == 0:
+        raise QlinError("qlin_kv_cache_bytes", 1)
+    return KVCache(_alloc_aligned(nbytes, device).zero_(), page, Hkv, D, k_scale, v_scale)
+
+
+def _ptr(t, name, dtype, device, shape=None):
+    """Address of a CUDA tensor on `device` (None for None): its dtype, last stride and shape checked."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != dtype or t.device != device:
+        raise TypeError(f"{name} must be a {dtype} tensor on {device}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    return t.data_ptr()
+
+
+def _rows(t, name, heads, D):
+    """(T, row stride) of T rows of heads * D contiguous values: (T, heads * D) or (T, heads, D)."""
+    if t.dim() == 3:
+        if t.shape[1] != heads or t.shape[2] != D or (heads > 1 and t.stride(1) != D):
+            raise ValueError(f"{name} must be (T, {heads}, {D}) with each row's heads contiguous")
+    elif t.dim() != 2 or t.shape[1] != heads * D:
+        raise ValueError(f"{name} must be (T, {heads * D}) or (T, {heads}, {D})")
+    T = t.shape[0]
+    return T, (t.stride(0) if T > 1 else heads * D)
+
+
+def _call(fn, device, stream, *args):
+    """fn(*args, stream) with `device` current (the library works on the current device)."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream must be on {device}")
+    if device.index == torch.cuda.current_device():
+        s = torch.cuda.current_stream(device) if stream is None else stream
+        st = getattr(lib(), fn)(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            s = torch.cuda.current_stream(device) if stream is None else stream
+            st = getattr(lib(), fn)(*args, s.cuda_stream)
+    _check(fn, st)
+
+
+def _qk_params(cos_sin, q_weight, k_weight, eps, rot, flags, D, device):
+    if cos_sin is None:
+        rot, n_pos = 0, 0
+    else:
+        rot = cos_sin.shape[-1] if rot is None else rot
+        n_pos = cos_sin.shape[0]
+    if cos_sin is not None and rot and (cos_sin.dim() != 2 or not cos_sin.is_contiguous()):
+        raise ValueError("cos_sin must be a contiguous (positions, rot) tensor")
+    return QKParams(_ptr(q_weight, "q_weight", torch.float32, device, (D,)),
+                    _ptr(k_weight, "k_weight", torch.float32, device, (D,)),
+                    _ptr(cos_sin, "cos_sin", torch.float32, device, (n_pos, rot) if rot else None), n_pos, rot, flags, eps)
+
+
+def qlin_qk_norm_rope(x, Hq, Hkv, D, positions=None, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, rot=None,
+                      flags=QLIN_ROPE_HALVES, q=None, k=None, ydt=QLIN_BF16, ws=None, stream=None):
+    """Norm (where a weight is given) and rotation of the query and key heads at the front of x's rows
+    (T, >= (Hq + Hkv) * D).  Returns (q, k) as (T, heads, D); q and k may be x's own heads."""
+    xdt = _XDT.get(x.dtype)
+    if xdt is None or not x.is_cuda or x.dim() != 2 or x.shape[1] < (Hq + Hkv) * D or x.stride(1) != 1:
+        raise TypeError("x must be a float32 or bfloat16 CUDA tensor (T, >= (Hq + Hkv) * D) with contiguous rows")
+    dev, T = x.device, x.shape[0]
+    out = _YDT[ydt]
+    if q is None:
+        q = torch.empty(T, Hq, D, dtype=out, device=dev)
+    if k is None:
+        k = torch.empty(T, Hkv, D, dtype=out, device=dev)
+    if ws is None:
+        ws = workspace(256, dev)
+    Tq, ldq = _rows(q, "q", Hq, D)
+    Tk, ldk = _rows(k, "k", Hkv, D)
+    if Tq != T or Tk != T:
+        raise ValueError("q and k must have x's rows")
+    par = _qk_params(cos_sin, q_weight, k_weight, eps, rot, flags, D, dev)
+    _call("qlin_qk_norm_rope", dev, stream, x.data_ptr(), xdt, T, x.stride(0) if T > 1 else x.shape[1], Hq, Hkv, D,
+          ctypes.addressof(par), _ptr(positions, "positions", torch.int32, dev, (T,)), _ptr(q, "q", out, dev), ldq,
+          _ptr(k, "k", out, dev), ldk, ydt, 0, _ptr(ws, "ws", torch.uint8, dev), ws.numel())
+    return q, k
+
+
+def qlin_kv_append(cache, x, Hq, positions, slots, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, rot=None,
+                   flags=QLIN_ROPE_HALVES, q=None, ws=None, stream=None):
+    """Append the tokens of x's rows (T, (Hq + 2 Hkv) * D: [q | k | v], fp32 or bf16) to the cache at `slots`
+    (int32; -1: a padding row).  Returns the normed and rotated queries, (T, Hq, D) bf16."""
+    Hkv, D = cache.Hkv, cache.D
+    xdt = _XDT.get(x.dtype)
+    if xdt is None or not x.is_cuda or x.dim() != 2 or x.shape[1] != (Hq + 2 * Hkv) * D or x.stride(1) != 1:
+        raise TypeError("x must be a float32 or bfloat16 CUDA tensor (T, (Hq + 2 Hkv) * D) with contiguous rows")
+    dev, T = x.device, x.shape[0]
+    if cache.data.device != dev:
+        raise ValueError(f"the cache must be on {dev}")
+    if q is None:
+        q = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    if ws is None:
+        ws = workspace(256, dev)
+    Tq, ldq = _rows(q, "q", Hq, D)
+    if Tq != T:
+        raise ValueError("q must have x's rows")
+    par = _qk_params(cos_sin, q_weight, k_weight, eps, rot, flags, D, dev)
+    _call("qlin_kv_append", dev, stream, cache.ref, x.data_ptr(), xdt, T, x.stride(0) if T > 1 else x.shape[1], Hq,
+          ctypes.addressof(par), _ptr(positions, "positions", torch.int32, dev, (T,)),
+          _ptr(slots, "slots", torch.int32, dev, (T,)), _ptr(q, "q", torch.bfloat16, dev) if Hq else None, ldq, 0,
+          _ptr(ws, "ws", torch.uint8, dev), ws.numel())
+    return q
+
+
+def qlin_kv_gather(cache, slots, k=None, v=None, ydt=QLIN_BF16, ws=None, stream=None):
+    """The values that slots of the cache stand for: (k, v), each (T, Hkv, D) fp32 or bf16."""
+    dev, T = cache.data.device, slots.shape[0]
+    out, shape = _YDT[ydt], (slots.shape[0], cache.Hkv, cache.D)
+    if k is None:
+        k = torch.empty(shape, dtype=out, device=dev)
+    if v is None:
+        v = torch.empty(shape, dtype=out, device=dev)
+    if not k.is_contiguous() or not v.is_contiguous():
+        raise ValueError("k and v must be contiguous")
+    if ws is None:
+        ws = workspace(256, dev)
+    _call("qlin_kv_gather", dev, stream, cache.ref, T, _ptr(slots, "slots", torch.int32, dev, (T,)),
+          _ptr(k, "k", out, dev, shape), _ptr(v, "v", out, dev, shape), ydt, _ptr(ws, "ws", torch.uint8, dev), ws.numel())
+    return k, v
+
+
+def qlin_attn_kv4_workspace_bytes(cache, B, max_q, Hq):
+    return lib().qlin_attn_kv4_workspace_bytes(cache.ref, B, max_q, Hq)
+
+
+def qlin_attn_kv4(cache, q, block_table, seq_lens, cu_q, max_q, scale=None, window=0, out=None, ws=None, stream=None):
+    """Causal attention of B sequences' last tokens over the cache.  q: (total_q, Hq, D) bf16; block_table: (B,
+    pages) int32; seq_lens: (B,) int32, each context with the call's own tokens; cu_q: (B + 1,) int32, the
+    sequences' first rows of q; max_q: the most queries of one sequence.  Returns out, q's shape, bf16."""
+    if q.dim() != 3 or q.shape[2] != cache.D:
+        raise ValueError(f"q must be (total_q, Hq, {cache.D})")
+    dev, D, Hq, B = q.device, cache.D, q.shape[1], seq_lens.shape[0]
+    if cache.data.device != dev:
+        raise ValueError(f"the cache must be on {dev}")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be (B, pages)")
+    total, ldq = _rows(q, "q", Hq, D)
+    if out is None:
+        out = torch.empty(total, Hq, D, dtype=torch.bfloat16, device=dev)
+    to, ldo = _rows(out, "out", Hq, D)
+    if to != total:
+        raise ValueError("out must have q's rows")
+    if ws is None:
+        ws = workspace(qlin_attn_kv4_workspace_bytes(cache, B, max_q, Hq), dev)
+    pages = block_table.shape[1]
+    _call("qlin_attn_kv4", dev, stream, cache.ref, _ptr(q, "q", torch.bfloat16, dev), ldq,
+          _ptr(block_table, "block_table", torch.int32, dev), block_table.stride(0) if B > 1 else pages, pages,
+          _ptr(seq_lens, "seq_lens", torch.int32, dev), _ptr(cu_q, "cu_q", torch.int32, dev, (B + 1,)), B, max_q, total,
+          Hq, D ** -0.5 if scale is None else scale, window, _ptr(out, "out", torch.bfloat16, dev), ldo, 0,
+          _ptr(ws, "ws", torch.uint8, dev), ws.numel())
+    return out

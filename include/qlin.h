@@ -381,6 +381,123 @@ qlin_status_t qlin_act_quant_mx_debug(const void* x, int M, int64_t K, int64_t l
 qlin_status_t qlin_dequant_debug(qlin_format_t fmt, const void* packed, int64_t N, int64_t K,
                                  int pack_flags, float* w, qlin_stream_t stream);
 
+/* ------------------------------------------------------------------------- queries, keys and the 4-bit cache */
+
+/* What stands between a decode step's fused qkv projection and its o projection: the norm and the
+ * rotation of queries and keys, the append of keys and values to a paged cache held in NVFP4, and
+ * the attention that reads it.  The pages describe such a cache (imp README, "Features" table: a
+ * paged KV cache in NVFP4 among its types) and name neither its layout nor its quantization; the
+ * layout is stated below, the quantization is the chunk path's NVFP4 rule with a given per-tensor
+ * scale.
+ *
+ * The cache is one buffer of pages [n_pages][Hkv][page / 16] of groups.  A group holds 16 tokens
+ * of one kv head in 18 * D bytes; token r (0..15) and value d of the head sit at
+ *   K codes  : byte r * D / 2 + d / 2, the even value in the low nibble
+ *   K scales : byte 8 D + r * D / 16 + d / 16             (E4M3, one per 16 values)
+ *   V codes  : byte 9 D + (d / 16) * 128 + r * 8 + (d % 16) / 2, the even value in the low nibble
+ *   V scales : byte 17 D + (d / 16) * 16 + r              (E4M3, one per 16 values)
+ * and the value is e2m1 * e4m3 * k_scale (v_scale).  Slot s of the cache is token s % page of page
+ * s / page. */
+typedef struct qlin_kv_cache {
+    void* data;             /* qlin_kv_cache_bytes(n_pages, page, Hkv, D) bytes, 256-byte aligned     */
+    int64_t n_pages;        /* n_pages * page < 2^31                                                  */
+    int32_t page;           /* tokens a page: 16, 32, 64, 128 or 256                                  */
+    int32_t Hkv;            /* key / value heads, 1 .. 1024                                           */
+    int32_t D;              /* values a head: 64 or 128 (else QLIN_ERR_UNSUPPORTED)                   */
+    float k_scale, v_scale; /* per-tensor scales, finite and > 0                                      */
+} qlin_kv_cache;
+
+/* Bytes of a cache's buffer (0 for invalid arguments). */
+size_t qlin_kv_cache_bytes(int64_t n_pages, int page, int Hkv, int D);
+
+enum {
+    QLIN_ROPE_HALVES = 0,     /* value i of the rotated part pairs with value i + rot / 2              */
+    QLIN_ROPE_INTERLEAVED = 1 /* value 2 i pairs with value 2 i + 1                                    */
+};
+
+/* How queries and keys are normed and rotated.  Per head h of D values:
+ *   n = h * w / sqrt(mean(h^2) + eps), or n = h where the weight is NULL;
+ *   the first rot values of n in pairs i: (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i), with the
+ *   cosines and sines of the token's position from cos_sin; the other values stay. */
+typedef struct qlin_qk_params {
+    const float* q_weight; /* D fp32 values, 16-byte aligned, or NULL: queries are not normed         */
+    const float* k_weight; /* the same for keys                                                       */
+    const float* cos_sin;  /* n_pos rows of rot fp32 values, 16-byte aligned: rot / 2 cosines, then
+                              rot / 2 sines; may be NULL where rot is 0                                */
+    int64_t n_pos;
+    int32_t rot;           /* rotated values a head: a multiple of 16, 0 <= rot <= D                  */
+    int32_t flags;         /* QLIN_ROPE_HALVES or QLIN_ROPE_INTERLEAVED                               */
+    float eps;             /* finite, >= 0                                                            */
+} qlin_qk_params;
+
+/* Norm and rotation of T tokens' queries and keys in one pass.
+ *   x : T rows [Hq heads of queries | Hkv heads of keys | anything], fp32 or bf16 (xdt), row stride
+ *       ldx elements, 16-byte aligned rows (ldx a multiple of 4 (fp32) or 8 (bf16))
+ *   positions : T int32, the tokens' rows of cos_sin; not read where rot is 0
+ *   q, k : T rows of Hq * D and Hkv * D values, fp32 or bf16 (ydt), row strides ldq and ldk elements,
+ *       rows aligned as x's; the arithmetic is fp32, rounded once.  q and k may overwrite x's
+ *       own heads (q = x, k = x + Hq * D, the same strides and type), and nothing else of x.
+ *   ws : 256 bytes (the status word), zero-filled before first use
+ * T = 0 does nothing.  A position outside [0, n_pos) leaves its token's q and k rows unwritten and
+ * sets the status word (qlin_ws_status: QLIN_ERR_INVALID_ARG). */
+qlin_status_t qlin_qk_norm_rope(const void* x, qlin_dtype_t xdt, int64_t T, int64_t ldx, int Hq, int Hkv, int D,
+                                const qlin_qk_params* params, const int32_t* positions, void* q, int64_t ldq, void* k,
+                                int64_t ldk, qlin_dtype_t ydt, int flags, void* ws, size_t ws_bytes,
+                                qlin_stream_t stream);
+
+/* Append T tokens to the cache: keys normed and rotated as above, then keys and values quantized to
+ * NVFP4 and written to the tokens' slots; the normed and rotated queries come out in bf16.
+ *   x : T rows [Hq heads of queries | Hkv of keys | Hkv of values], types and strides as above (the
+ *       output row of a fused qkv projection)
+ *   slots : T int32, each token's place in the cache (distinct); -1 writes nothing of the token,
+ *       neither cache nor q (a padding row)
+ *   q : T rows of Hq * D bf16, row stride ldq, 16-byte aligned rows; NULL (Hq = 0 allowed): not written
+ * Quantization, with g the cache's scale and every step in fp32, round to nearest even:
+ *   s_b = E4M3_satfinite(amax_b / (6 g)) per 16 values, code = E2M1_satfinite(x / (e4m3(s_b) g)), 0
+ *   where that divisor is 0.
+ * A key's fp32 value is the 64-bit result rounded once, so that its code does not depend on the order of
+ * a sum: the same token gives the same bytes appended alone or in a chunk.  Infinite inputs saturate;
+ * NaN inputs give some finite value.  Other slots of the cache are left as they are.
+ * Errors as above; a position outside [0, n_pos) or a slot outside [-1, n_pages * page) leaves the
+ * token unwritten and sets the status word. */
+qlin_status_t qlin_kv_append(const qlin_kv_cache* cache, const void* x, qlin_dtype_t xdt, int64_t T, int64_t ldx,
+                             int Hq, const qlin_qk_params* params, const int32_t* positions, const int32_t* slots,
+                             void* q, int64_t ldq, int flags, void* ws, size_t ws_bytes, qlin_stream_t stream);
+
+/* The values that T slots of the cache stand for: fp32(e2m1 * e4m3 * scale), one rounding (bf16: a
+ * second).  k, v: T x Hkv * D, contiguous, 16-byte aligned, fp32 or bf16 (ydt).  Slot -1 leaves its
+ * rows unwritten; a slot outside [-1, n_pages * page) also sets the status word.  ws: 256 bytes. */
+qlin_status_t qlin_kv_gather(const qlin_kv_cache* cache, int64_t T, const int32_t* slots, void* k, void* v,
+                             qlin_dtype_t ydt, void* ws, size_t ws_bytes, qlin_stream_t stream);
+
+/* Workspace bytes of qlin_attn_kv4 for these arguments on the current device (0 if invalid). */
+size_t qlin_attn_kv4_workspace_bytes(const qlin_kv_cache* cache, int B, int max_q, int Hq);
+
+/* Attention of B sequences' last tokens over the paged cache:
+ *   out = softmax(scale * q K^T) V, per query head, with query head h reading kv head h / (Hq / Hkv).
+ * Sequence b has n = cu_q[b+1] - cu_q[b] queries, rows cu_q[b] .. of q and out, and a context of
+ * L = seq_lens[b] tokens that counts the call's own (append them first): query i stands at place
+ * p = L - n + i and sees the places t <= p, with window > 0 only those with t > p - window.  A query
+ * that sees nothing (p < 0) gives a row of zeros.  Single tokens (n = 1) and prompt chunks are the same
+ * call.  What the cache holds behind a sequence's end is never used, whatever its bits.
+ *   q, out : total_q rows of Hq * D bf16, row strides ldq and ldo elements, 16-byte aligned rows; rows
+ *       outside cu_q[0] .. cu_q[B] are left as they are.  The products are exact values of K and V
+ *       with q and with probabilities in fp16; scores, softmax sums and outputs are fp32, rounded once.
+ *   block_table : B rows of int32 page numbers, row stride ldb, max_pages columns: token t of sequence b
+ *       is token t % page of page block_table[b * ldb + t / page]
+ *   seq_lens : B int32; cu_q : B + 1 int32; both device arrays, so one captured graph serves any lengths
+ *   max_q : the most queries of one sequence in this call (it sizes the grid); Hq a multiple of Hkv,
+ *       Hq / Hkv <= 64; B <= 1024
+ *   ws : qlin_attn_kv4_workspace_bytes(cache, B, max_q, Hq) bytes, zero-filled before first use; it may
+ *       be reused by any later qlin_attn_kv4 call on the same stream for which it is large enough
+ * A sequence with n outside [0, max_q], rows outside [0, total_q) or L outside [0, max_pages * page] is
+ * skipped; a page number outside [0, n_pages) counts as masked places.  Both set the status word
+ * (QLIN_ERR_INVALID_ARG).  Results are the same from run to run. */
+qlin_status_t qlin_attn_kv4(const qlin_kv_cache* cache, const void* q, int64_t ldq, const int32_t* block_table,
+                            int64_t ldb, int max_pages, const int32_t* seq_lens, const int32_t* cu_q, int B,
+                            int max_q, int64_t total_q, int Hq, float scale, int window, void* out, int64_t ldo,
+                            int flags, void* ws, size_t ws_bytes, qlin_stream_t stream);
+
 /* Read and clear the sticky device status word of a workspace (synchronises `stream`).
  * Returns QLIN_OK, QLIN_ERR_TIMEOUT if a bounded device wait gave up since the last check, or
  * QLIN_ERR_INVALID_ARG if qlin_moe_experts met an invalid or repeated expert id. */

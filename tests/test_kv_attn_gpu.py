@@ -1,0 +1,512 @@
+"""The query / key norm and rotation, the append to the paged NVFP4 cache, its read-back and the attention over it,
+against plain 64-bit forms (kv_reference.py), at the sizes, masks and layouts where they can go wrong."""
+import pytest
+import torch
+
+import gemm_dequant_gemv_q8_b200 as q
+import kv_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+# ----------------------------------------------------------------------------- norm and rotation
+# 32-bit arithmetic: the sum of squares (13 roundings, halved by the root), root, quotient, two products, the
+# rotation's two: 14 of them at most; 16 are allowed, of the magnitudes behind the value, and the output's own half step.
+def rope_tol(y, A, dtype):
+    t = 16 * 2.0 ** -24 * A
+    return t + (torch.finfo(dtype).eps / 2) * (y.abs() + t) + 1e-38
+
+
+ROPE = [  # T, Hq, Hkv, D, rot, interleaved, norm, x, y
+    (1, 32, 8, 128, 128, False, True, F32, BF16),
+    (3, 5, 1, 64, 64, True, True, F32, F32),
+    (17, 3, 3, 128, 64, True, True, BF16, F32),
+    (33, 6, 2, 64, 32, False, True, BF16, BF16),
+    (129, 16, 4, 128, 16, False, False, F32, F32),
+    (7, 1, 1, 64, 0, False, True, BF16, F32),
+    (300, 9, 3, 128, 128, False, True, BF16, BF16),
+]
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,inter,norm,xdt,ydt", ROPE)
+def test_norm_rope(T, Hq, Hkv, D, rot, inter, norm, xdt, ydt):
+    g = gen(T + D)
+    extra = 8  # rows wider than the heads: a stride of their own
+    x = (torch.randn(T, (Hq + Hkv) * D + extra, generator=g) * torch.exp(torch.randn(T, 1, generator=g))).to(xdt)
+    x[0] = 0  # a head of zeros: eps alone keeps it finite
+    w = [1 + 0.3 * torch.randn(D, generator=g) for _ in range(2)] if norm else [None, None]
+    pos = torch.randint(0, 5000, (T,), generator=g, dtype=torch.int32)
+    cs = ref.table(5000, rot) if rot else None
+    cu = lambda t: None if t is None else t.cuda()  # noqa: E731
+    ws = q.workspace(256)
+    qo, ko = q.qlin_qk_norm_rope(x.cuda(), Hq, Hkv, D, pos.cuda(), cu(cs), cu(w[0]), cu(w[1]), 1e-6,
+                                 flags=q.QLIN_ROPE_INTERLEAVED if inter else 0,
+                                 ydt=q.QLIN_F32 if ydt == F32 else q.QLIN_BF16, ws=ws)
+    assert q.qlin_ws_status(ws) == 0
+    xd = x[:, :(Hq + Hkv) * D].double().view(T, Hq + Hkv, D)
+    for got, part, wt in ((qo, xd[:, :Hq], w[0]), (ko, xd[:, Hq:], w[1])):
+        y, A = ref.norm_rope(part, wt, 1e-6, cs, pos, rot, inter)
+        assert ((got.cpu().double() - y).abs() <= rope_tol(y, A, ydt)).all()
+
+
+def test_norm_rope_in_place_and_strided_outputs():
+    T, Hq, Hkv, D = 37, 6, 2, 64
+    x = torch.randn(T, (Hq + 2 * Hkv) * D, generator=gen(5)).cuda()
+    pos, cs = torch.arange(T, dtype=torch.int32).cuda(), ref.table(64, D).cuda()
+    w = torch.ones(D).cuda()
+    a, b = q.qlin_qk_norm_rope(x, Hq, Hkv, D, pos, cs, w, w, ydt=q.QLIN_F32)
+    buf = torch.full((T, (Hq + Hkv) * D + 12), 7.0, device="cuda")
+    q.qlin_qk_norm_rope(x, Hq, Hkv, D, pos, cs, w, w, ydt=q.QLIN_F32, q=buf[:, :Hq * D],
+                        k=buf[:, Hq * D:(Hq + Hkv) * D])
+    assert torch.equal(buf[:, :Hq * D], a.flatten(1)) and torch.equal(buf[:, Hq * D:(Hq + Hkv) * D], b.flatten(1))
+    assert (buf[:, (Hq + Hkv) * D:] == 7).all()
+    v = x[:, (Hq + Hkv) * D:].clone()
+    q.qlin_qk_norm_rope(x, Hq, Hkv, D, pos, cs, w, w, ydt=q.QLIN_F32, q=x[:, :Hq * D], k=x[:, Hq * D:(Hq + Hkv) * D])
+    assert torch.equal(x[:, :Hq * D], a.flatten(1)) and torch.equal(x[:, Hq * D:(Hq + Hkv) * D], b.flatten(1))
+    assert torch.equal(x[:, (Hq + Hkv) * D:], v)
+
+
+def test_norm_rope_bad_positions_leave_their_rows():
+    T, Hq, Hkv, D = 5, 2, 1, 64
+    x = torch.randn(T, (Hq + Hkv) * D, generator=gen(6)).cuda()
+    cs = ref.table(10, D).cuda()
+    pos = torch.tensor([0, -1, 9, 10, 3], dtype=torch.int32).cuda()
+    qo = torch.full((T, Hq, D), 7.0, device="cuda")
+    ko = torch.full((T, Hkv, D), 7.0, device="cuda")
+    ws = q.workspace(256)
+    q.qlin_qk_norm_rope(x, Hq, Hkv, D, pos, cs, ydt=q.QLIN_F32, q=qo, k=ko, ws=ws)
+    assert q.qlin_ws_status(ws) == 1 and q.qlin_ws_status(ws) == 0
+    assert (qo[[1, 3]] == 7).all() and (ko[[1, 3]] == 7).all()
+    good = [0, 2, 4]
+    a, b = q.qlin_qk_norm_rope(x[good].contiguous(), Hq, Hkv, D, pos[good].contiguous(), cs, ydt=q.QLIN_F32)
+    assert torch.equal(qo[good], a) and torch.equal(ko[good], b)
+
+
+# ----------------------------------------------------------------------------- append and read-back
+APPEND = [  # T, Hq, Hkv, D, rot, interleaved, norm, x, page, ks, vs
+    (1, 32, 8, 128, 128, False, True, F32, 16, 1.0, 1.0),
+    (5, 0, 2, 64, 32, True, True, F32, 32, 0.37, 2.5),
+    (45, 4, 4, 128, 64, True, False, BF16, 64, 0.01, 0.3),
+    (130, 3, 1, 64, 64, False, True, BF16, 128, 3.0, 1.0),
+    (77, 16, 8, 128, 0, False, True, F32, 256, 1.0, 0.125),
+]
+
+
+def append_inputs(T, Hq, Hkv, D, rot, xdt, norm, page, seed):
+    g = gen(seed)
+    x = torch.randn(T, (Hq + 2 * Hkv) * D, generator=g) * torch.exp(torch.randn((Hq + 2 * Hkv) * D, generator=g))
+    x[T // 2, -D:-D + 16] = 0      # a block of zeros: scale 0, codes 0
+    x[0, -16:] *= 1e4              # a block that saturates its scale
+    x[T // 3, -32:-16] *= 1e-4     # a block below the smallest scale's reach
+    x = x.to(xdt)
+    w = [1 + 0.3 * torch.randn(D, generator=g) for _ in range(2)] if norm else [None, None]
+    pos = torch.randint(0, 3000, (T,), generator=g, dtype=torch.int32)
+    n_pages = T // page + 3
+    slots = torch.randperm(n_pages * page, generator=g)[:T].int()
+    return x, w, pos, ref.table(3000, rot) if rot else None, n_pages, slots
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,inter,norm,xdt,page,ks,vs", APPEND)
+def test_append_and_gather(T, Hq, Hkv, D, rot, inter, norm, xdt, page, ks, vs):
+    x, w, pos, cs, n_pages, slots = append_inputs(T, Hq, Hkv, D, rot, xdt, norm, page, T + page)
+    if T > 4:
+        slots[3] = -1
+    cu = lambda t: None if t is None else t.cuda()  # noqa: E731
+    before = torch.randint(0, 256, (q.qlin_kv_cache_bytes(n_pages, page, Hkv, D),), generator=gen(9), dtype=torch.uint8)
+    cache = q.kv_cache(n_pages, page, Hkv, D, ks, vs)
+    cache.data.copy_(before)
+    ws = q.workspace(256)
+    qo = torch.full((T, max(Hq, 1), D), 7.0, dtype=BF16, device="cuda")[:, :Hq]
+    q.qlin_kv_append(cache, x.cuda(), Hq, pos.cuda(), slots.cuda(), cu(cs), cu(w[0]), cu(w[1]), 1e-6,
+                     flags=q.QLIN_ROPE_INTERLEAVED if inter else 0, q=qo if Hq else None, ws=ws)
+    assert q.qlin_ws_status(ws) == 0
+    xd = x.double().view(T, Hq + 2 * Hkv, D)
+    live = slots >= 0
+    if Hq:
+        y, A = ref.norm_rope(xd[:, :Hq], w[0], 1e-6, cs, pos, rot, inter)
+        got = qo.cpu().double()
+        assert ((got - y).abs() <= rope_tol(y, A, BF16))[live].all()
+        assert (got[~live] == 7).all()
+    k, _ = ref.norm_rope(xd[:, Hq:Hq + Hkv], w[1], 1e-6, cs, pos, rot, inter)
+    kc, kb = ref.quantize(k.float(), ks)
+    vc, vb = ref.quantize(xd[:, Hq + Hkv:].float(), vs)
+    want = before.clone()
+    ref.put(want, page, Hkv, D, slots, kc, kb, vc, vb)
+    assert torch.equal(cache.data.cpu(), want)  # every other byte as it was
+    for dt, ydt in ((q.QLIN_F32, F32), (q.QLIN_BF16, BF16)):
+        gk, gv = q.qlin_kv_gather(cache, slots.cuda(), ydt=dt, ws=ws)
+        assert torch.equal(gk.cpu()[live], ref.values(kc, kb, ks).float().to(ydt)[live])
+        assert torch.equal(gv.cpu()[live], ref.values(vc, vb, vs).float().to(ydt)[live])
+    assert q.qlin_ws_status(ws) == 0
+
+
+def test_append_alone_gives_the_chunks_bytes():
+    T, Hq, Hkv, D, page = 40, 4, 2, 128, 16
+    x, w, pos, cs, n_pages, slots = append_inputs(T, Hq, Hkv, D, D, F32, True, page, 3)
+    xc, pc, sc, w, cs = x.cuda(), pos.cuda(), slots.cuda(), [t.cuda() for t in w], cs.cuda()
+    a, b = q.kv_cache(n_pages, page, Hkv, D), q.kv_cache(n_pages, page, Hkv, D)
+    qa = q.qlin_kv_append(a, xc, Hq, pc, sc, cs, *w)
+    qb = torch.cat([q.qlin_kv_append(b, xc[t:t + 1], Hq, pc[t:t + 1], sc[t:t + 1], cs, *w) for t in range(T)])
+    assert torch.equal(a.data, b.data) and torch.equal(qa, qb)
+
+
+def test_append_edge_values():
+    # exact ties of the code's and the scale's rounding, infinities, the largest finite value, both zeros
+    D, page = 64, 16
+    x = torch.zeros(8, 2 * D)
+    x[0, D:D + 16] = torch.tensor([6, 5, 3.5, 2.5, 1.75, 1.25, 0.75, 0.25, -6, -5, -3.5, -2.5, -1.75, -1.25, -0.75, -0.25])
+    x[1, D:D + 16] = x[0, D:D + 16] * 17 / 16    # the scale is a tie of E4M3
+    x[2, D:D + 16] = x[0, D:D + 16] * 2.0 ** -10  # the scale is half the smallest
+    x[3, D:D + 16] = x[0, D:D + 16] * 3e38 / 6
+    x[4, D] = float("inf")
+    x[4, D + 1] = -1.0
+    x[5, D] = -0.0
+    x[6, D:] = 1e-40
+    x[7, :D] = torch.arange(D) - 31.0
+    cache = q.kv_cache(1, page, 1, D)
+    slots = torch.arange(8, dtype=torch.int32)
+    q.qlin_kv_append(cache, x.cuda(), 0, None, slots.cuda(), None, q=None)
+    kc, kb = ref.quantize(x[:, :D].view(8, 1, D), 1.0)
+    vc, vb = ref.quantize(x[:, D:].view(8, 1, D), 1.0)
+    k, v = q.qlin_kv_gather(cache, slots.cuda(), ydt=q.QLIN_F32)
+    assert torch.equal(k.cpu(), ref.values(kc, kb).float())
+    assert torch.equal(v.cpu()[[0, 1, 2, 3, 5, 6, 7]], ref.values(vc, vb).float()[[0, 1, 2, 3, 5, 6, 7]])
+    assert v[4, 0, 0].item() == 6 * 448 and v[4, 0, 1].item() == 0
+
+
+def test_append_bad_slots_and_positions():
+    T, Hq, Hkv, D, page = 6, 1, 1, 64, 16
+    x = torch.randn(T, 3 * D, generator=gen(8)).cuda()
+    cs = ref.table(10, D).cuda()
+    cache = q.kv_cache(2, page, Hkv, D)
+    pos = torch.tensor([0, 1, 2, 10, 4, -3], dtype=torch.int32).cuda()
+    slots = torch.tensor([0, 32, -2, 3, 31, 5], dtype=torch.int32).cuda()
+    ws = q.workspace(256)
+    qo = torch.full((T, Hq, D), 7.0, dtype=BF16, device="cuda")
+    q.qlin_kv_append(cache, x, Hq, pos, slots, cs, q=qo, ws=ws)
+    assert q.qlin_ws_status(ws) == 1
+    assert (qo[[1, 2, 3, 5]] == 7).all() and (qo[[0, 4]] != 7).any()
+    want = q.kv_cache(2, page, Hkv, D)
+    q.qlin_kv_append(want, x[[0, 4]].contiguous(), Hq, pos[[0, 4]].contiguous(), slots[[0, 4]].contiguous(), cs)
+    assert torch.equal(cache.data, want.data)
+    k, v = torch.full((T, Hkv, D), 7.0, device="cuda"), torch.full((T, Hkv, D), 7.0, device="cuda")
+    q.qlin_kv_gather(cache, slots, k=k, v=v, ydt=q.QLIN_F32, ws=ws)
+    assert q.qlin_ws_status(ws) == 1
+    assert (k[[1, 2]] == 7).all() and (v[[1, 2]] == 7).all() and (k[[0, 4]] != 7).any()
+
+
+# ----------------------------------------------------------------------------- attention
+def attn_case(lens, nqs, Hq, Hkv, D, page, seed, spare=2, junk=True, k_size=1.0):
+    """Sequences on random pages.  What lies behind each sequence's end is junk: NaN scales, any codes."""
+    g = gen(seed)
+    need = [-(-L // page) for L in lens]
+    n_pages = sum(need) + spare
+    cache, k, v = ref.random_cache(n_pages, page, Hkv, D, g, k_size=k_size)
+    order = torch.randperm(n_pages, generator=g)
+    width = max(max(need), 1) + 1
+    table = torch.full((len(lens), width), n_pages - 1, dtype=torch.int32)
+    at, ks, vs = 0, [], []
+    c = cache.view(n_pages, Hkv, page // 16, 18 * D)
+    used = set()
+    for b, n in enumerate(need):
+        ids = order[at:at + n]
+        at += n
+        table[b, :n] = ids.int()
+        used |= set(ids.tolist())
+        idx = (ids[:, None] * page + torch.arange(page)).flatten()[:lens[b]]
+        ks.append(k[idx])
+        vs.append(v[idx])
+        if junk and lens[b] % page:
+            last = c[ids[-1]]
+            for t in range(lens[b] % page, page):
+                gr, r = last[:, t // 16], t % 16
+                gr[:, 8 * D + r * (D // 16):8 * D + (r + 1) * (D // 16)] = 0x7F
+                gr[:, r * (D // 2):(r + 1) * (D // 2)] = 0xA5
+                gr[:, 17 * D + r::16] = 0xFF
+    if junk:
+        for p in set(range(n_pages)) - used:
+            c[p] = 0x7F
+    qs = [(1.5 * torch.randn(n, Hq, D, generator=g)).bfloat16() for n in nqs]
+    cu = torch.tensor([0] + torch.tensor(nqs).cumsum(0).tolist(), dtype=torch.int32)
+    return cache, table, torch.tensor(lens, dtype=torch.int32), cu, qs, ks, vs
+
+
+def run_attn(cache, page, Hkv, D, table, lens, cu, qs, max_q=None, scale=None, window=0, ks=1.0, vs=1.0, ws=None, out=None):
+    kv = q.KVCache(dev_cache(cache), page, Hkv, D, ks, vs)
+    qq = torch.cat(qs).cuda()
+    mq = max(len(t) for t in qs) if max_q is None else max_q
+    if ws is None:
+        ws = q.workspace(q.qlin_attn_kv4_workspace_bytes(kv, len(lens), mq, qq.shape[1]))
+    o = q.qlin_attn_kv4(kv, qq, table.cuda(), lens.cuda(), cu.cuda(), mq, scale, window=window, ws=ws, out=out)
+    return o, q.qlin_ws_status(ws)
+
+
+def dev_cache(cache):
+    d = q._alloc_aligned(cache.numel(), "cuda")
+    return d.copy_(cache)
+
+
+def check_attn(o, lens, cu, qs, ks, vs, D, scale, window=0, kscale=1.0, vscale=1.0):
+    o = o.cpu().double()
+    for b, L in enumerate(lens.tolist()):
+        out, tp, ts, tv = ref.attention(qs[b].double(), ks[b] * kscale, vs[b] * vscale, L, scale, window)
+        got = o[cu[b]:cu[b + 1]]
+        tol = ref.attention_tol(out, tp, ts, tv, D, L)
+        err = (got - out).abs()
+        assert (err <= tol + 1e-30).all(), (b, L, float((err / (tol + 1e-30)).max()))
+
+
+DECODE = [  # lens, Hq, Hkv, D, page, window
+    ([1], 1, 1, 64, 16, 0),
+    ([1, 2, 15, 16, 17, 31, 32, 33], 8, 2, 128, 16, 0),
+    ([63, 64, 65, 127, 128, 129, 0, 300], 6, 2, 64, 64, 0),
+    ([1000, 3, 517], 32, 8, 128, 32, 0),
+    ([2500], 5, 1, 128, 128, 0),
+    ([700, 44], 16, 2, 64, 256, 0),
+    ([900, 77, 1], 4, 4, 128, 16, 100),
+    ([640, 641], 16, 1, 128, 64, 1),
+    ([333, 12], 40, 2, 128, 16, 0),
+    ([257], 64, 1, 64, 16, 33),
+]
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,page,window", DECODE)
+def test_decode(lens, Hq, Hkv, D, page, window):
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, [1] * len(lens), Hq, Hkv, D, page, Hq + D + page)
+    o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs, window=window)
+    assert st == 0
+    check_attn(o, ln, cu, qs, ks, vs, D, D ** -0.5, window)
+
+
+CHUNK = [  # lens, queries, Hq, Hkv, D, page, window
+    ([2], [2], 2, 1, 64, 16, 0),
+    ([40, 9, 200], [4, 3, 1], 8, 2, 128, 16, 0),
+    ([100, 7], [5, 7], 6, 2, 64, 32, 0),
+    ([128], [128], 4, 1, 128, 64, 0),
+    ([129], [127], 4, 2, 128, 16, 0),
+    ([513, 300, 64], [200, 300, 1], 8, 2, 128, 64, 0),
+    ([700, 260], [257, 31], 6, 2, 64, 16, 0),
+    ([600], [320], 5, 1, 128, 128, 0),
+    ([640, 385], [300, 129], 8, 1, 64, 32, 70),
+    ([900], [150], 3, 3, 128, 16, 333),
+    ([400], [90], 64, 1, 64, 16, 0),
+    ([50, 0, 3], [60, 4, 9], 4, 2, 128, 16, 0),   # more queries than tokens: the first see nothing
+    ([333, 20], [0, 20], 8, 4, 128, 32, 0),       # a sequence without queries
+]
+
+
+@pytest.mark.parametrize("lens,nqs,Hq,Hkv,D,page,window", CHUNK)
+def test_chunk(lens, nqs, Hq, Hkv, D, page, window):
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, nqs, Hq, Hkv, D, page, Hq + D + page + sum(nqs))
+    o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs, window=window)
+    assert st == 0
+    check_attn(o, ln, cu, qs, ks, vs, D, D ** -0.5, window)
+
+
+@pytest.mark.parametrize("nq", [1, 70])
+def test_attention_scales_and_sharp_scores(nq):
+    # scores up to some hundreds: one token takes nearly all; scales other than 1; a scale argument
+    lens, Hq, Hkv, D, page = [700, 333], 8, 2, 128, 32
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, [nq, nq], Hq, Hkv, D, page, 77, k_size=8.0)
+    o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs, scale=0.25, ks=0.5, vs=3.0)
+    assert st == 0
+    check_attn(o, ln, cu, qs, ks, vs, D, 0.25, kscale=0.5, vscale=3.0)
+
+
+@pytest.mark.parametrize("nq", [1, 70])
+def test_attention_rising_and_falling_scores(nq):
+    # the running maximum moves at every tile, or never: keys along one query, growing or shrinking with the place
+    Hq, Hkv, D, page, L = 2, 1, 64, 16, 600
+    g = gen(4)
+    d = torch.randn(D, generator=g)
+    for up in (True, False):
+        f = torch.arange(L).float() / L * 6
+        f = f if up else f.flip(0)
+        kc, kb = ref.quantize((f[:, None] * d)[:, None], 1.0)
+        vc, vb = ref.quantize(torch.randn(L, 1, D, generator=g), 1.0)
+        n_pages = -(-L // page)
+        c = torch.zeros(q.qlin_kv_cache_bytes(n_pages, page, 1, D), dtype=torch.uint8)
+        ref.put(c, page, 1, D, torch.arange(L), kc, kb, vc, vb)
+        qs = [(d * torch.ones(nq, Hq, 1)).bfloat16()]
+        table = torch.arange(n_pages, dtype=torch.int32)[None]
+        cu = torch.tensor([0, nq], dtype=torch.int32)
+        ln = torch.tensor([L], dtype=torch.int32)
+        o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs)
+        assert st == 0
+        check_attn(o, ln, cu, qs, [ref.values(kc, kb)], [ref.values(vc, vb)], D, D ** -0.5)
+
+
+@pytest.mark.parametrize("nq", [1, 70])
+def test_attention_query_sizes(nq):
+    # queries far outside fp16's range, rows of zeros beside them; q and out as strided views
+    lens, Hq, Hkv, D, page = [200], 4, 2, 64, 16
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, [nq], Hq, Hkv, D, page, 78)
+    big = qs[0].clone()
+    big[:, 0] *= 1e30
+    big[:, 1] *= 1e-30
+    big[:, 2] = 0
+    kv = q.KVCache(dev_cache(c), page, Hkv, D)
+    wide = torch.zeros(nq, Hq * D + 64, dtype=BF16, device="cuda")
+    qv = wide[:, :Hq * D].unflatten(1, (Hq, D))
+    qv.copy_(big.cuda())
+    ob = torch.full((nq + 3, Hq * D + 8), 7.0, dtype=BF16, device="cuda")
+    q.qlin_attn_kv4(kv, qv, table.cuda(), ln.cuda(), cu.cuda(), nq, 1e-2, out=ob[:nq, :Hq * D].unflatten(1, (Hq, D)))
+    assert (ob[nq:] == 7).all() and (ob[:, Hq * D:] == 7).all()
+    o = ob[:nq, :Hq * D].unflatten(1, (Hq, D))
+    # scores of 1e28: the largest one takes all, so the row is that token's V
+    out, tp, ts, tv = ref.attention(big.double(), ks[0], vs[0], 200, 1e-2)
+    got = o.cpu().double()
+    for h in (1, 2, 3):
+        tol = ref.attention_tol(out, tp, ts, tv, D, 200)[:, h]
+        assert ((got[:, h] - out[:, h]).abs() <= tol).all()
+    assert ((got[:, 0] - out[:, 0]).abs() <= 2.0 ** -8 * out[:, 0].abs() + 2.0 ** -10).all()
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_attention_rows_behind_the_last_sequence_stay(nq):
+    lens, Hq, Hkv, D, page = [90, 33], 8, 2, 64, 16
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, [nq, nq], Hq, Hkv, D, page, 79)
+    pad = torch.full((5, Hq, D), float("nan"), dtype=BF16)
+    out = torch.full((2 * nq + 5, Hq, D), 7.0, dtype=BF16, device="cuda")
+    run_attn(c, page, Hkv, D, table, ln, cu, [*qs, pad], max_q=nq, out=out)
+    assert (out[2 * nq:] == 7).all()
+    check_attn(out, ln, cu, qs, ks, vs, D, D ** -0.5)
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_attention_bad_sequences_are_skipped(nq):
+    lens, Hq, Hkv, D, page = [90, 60, 33, 50], 8, 2, 64, 16
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, [nq] * 4, Hq, Hkv, D, page, 80)
+    bad = ln.clone()
+    bad[1] = -5
+    bad[3] = 10 ** 9
+    out = torch.full((4 * nq, Hq, D), 7.0, dtype=BF16, device="cuda")
+    o, st = run_attn(c, page, Hkv, D, table, bad, cu, qs, out=out)
+    assert st == 1
+    assert (o[nq:2 * nq] == 7).all() and (o[3 * nq:] == 7).all()
+    keep = [0, 2]
+    for b in keep:
+        got = o[b * nq:(b + 1) * nq].cpu().double()
+        ref_out, tp, ts, tv = ref.attention(qs[b].double(), ks[b], vs[b], lens[b], D ** -0.5)
+        assert ((got - ref_out).abs() <= ref.attention_tol(ref_out, tp, ts, tv, D, lens[b])).all()
+    # a page number outside the cache: its tokens count as masked
+    t2 = table.clone()
+    t2[0, 1] = 10 ** 6
+    t2[2, 0] = -1
+    o, st = run_attn(c, page, Hkv, D, t2, ln, cu, qs)
+    assert st == 1
+    i = torch.cat([torch.arange(16), torch.arange(32, 90)])
+    if nq == 1:
+        ref_out, tp, ts, tv = ref.attention(qs[0].double(), ks[0][i], vs[0][i], 74, D ** -0.5)
+        assert ((o[:1].cpu().double() - ref_out).abs() <= ref.attention_tol(ref_out, tp, ts, tv, D, 90)).all()
+
+
+@pytest.mark.parametrize("nq", [1, 64])
+def test_attention_repeats_replays_and_streams(nq):
+    # the same bits again, on a dirty workspace, from a captured graph with new lengths, and on another stream
+    Hq, Hkv, D, page = 8, 2, 128, 16
+    lens = [800, 90, 371]
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, [nq] * 3, Hq, Hkv, D, page, 81)
+    kv = q.KVCache(dev_cache(c), page, Hkv, D)
+    qq, tb, l2, cc = torch.cat(qs).cuda(), table.cuda(), ln.cuda(), cu.cuda()
+    ws = q.workspace(q.qlin_attn_kv4_workspace_bytes(kv, 3, nq, Hq))
+    a = q.qlin_attn_kv4(kv, qq, tb, l2, cc, nq, ws=ws)
+    out = torch.empty_like(a)
+    for _ in range(3):
+        q.qlin_attn_kv4(kv, qq, tb, l2, cc, nq, ws=ws, out=out)
+        assert torch.equal(out, a)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        q.qlin_attn_kv4(kv, qq, tb, l2, cc, nq, ws=ws, out=out)
+        assert torch.equal(out, a)
+        with torch.cuda.graph(graph, stream=side):
+            q.qlin_attn_kv4(kv, qq, tb, l2, cc, nq, ws=ws, out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    for new in ([800, 90, 371], [nq, 700, 1 + nq], [12, 0, 371]):
+        fit = [min(n, len(tb[0]) * page, -(-len(k) // page) * page) for n, k in zip(new, ks)]
+        fit = [min(n, len(k)) for n, k in zip(fit, ks)]
+        l2.copy_(torch.tensor(fit, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        check_attn(out, torch.tensor(fit), cu, qs, [k[:n] for k, n in zip(ks, fit)], [v[:n] for v, n in zip(vs, fit)], D,
+                   D ** -0.5)
+    assert q.qlin_ws_status(ws) == 0
+
+
+@pytest.mark.parametrize("nq", [1, 20])
+def test_attention_cache_beyond_32_bits(nq):
+    # byte offsets past 2^32: the sequence's pages lie at the end of a 4.4 GB cache
+    Hq, Hkv, D, page, L = 8, 8, 128, 256, 500
+    per = q.qlin_kv_cache_bytes(1, page, Hkv, D)
+    n_pages = (1 << 32) // per + 40
+    small, k, v = ref.random_cache(2, page, Hkv, D, gen(82))
+    data = q._alloc_aligned(n_pages * per, "cuda")
+    data[-2 * per:].copy_(small)
+    kv = q.KVCache(data, page, Hkv, D)
+    table = torch.tensor([[n_pages - 1, n_pages - 2]], dtype=torch.int32)
+    k, v = torch.cat([k[page:], k[:page]])[:L], torch.cat([v[page:], v[:page]])[:L]
+    qs = torch.randn(nq, Hq, D, generator=gen(83)).bfloat16()
+    ln, cu = torch.tensor([L], dtype=torch.int32), torch.tensor([0, nq], dtype=torch.int32)
+    o = q.qlin_attn_kv4(kv, qs.cuda(), table.cuda(), ln.cuda(), cu.cuda(), nq)
+    check_attn(o, ln, cu, [qs], [k], [v], D, D ** -0.5)
+    # and the append and read-back at the last slot
+    x = torch.randn(1, 2 * Hkv * D, generator=gen(84))
+    last = torch.tensor([n_pages * page - 1], dtype=torch.int32).cuda()
+    q.qlin_kv_append(kv, x.cuda(), 0, None, last, None)
+    gk, _ = q.qlin_kv_gather(kv, last, ydt=q.QLIN_F32)
+    kc, kb = ref.quantize(x[:, :Hkv * D].view(1, Hkv, D), 1.0)
+    assert torch.equal(gk.cpu(), ref.values(kc, kb).float())
+
+
+# ----------------------------------------------------------------------------- as they are used
+def test_decode_step_from_qkv_projection_to_o_projection():
+    """Prompt and decode steps of one attention layer: the Q4_0 qkv projection, the append, the attention, the o
+    projection; every step's attention output against the 64-bit form of the same projections' outputs."""
+    import synth
+    H, Hq, Hkv, D, page, B = 512, 8, 2, 64, 16, 2
+    W = (Hq + 2 * Hkv) * D
+    qkv_w = q.qlin_pack_weights(q.QLIN_Q4_0, W, H, synth.weights(q.QLIN_Q4_0, W, H, synth.gen(1))[0].cuda())
+    o_w = q.qlin_pack_weights(q.QLIN_Q4_0, H, Hq * D, synth.weights(q.QLIN_Q4_0, H, Hq * D, synth.gen(2))[0].cuda())
+    cs = ref.table(200, D)
+    w = [1 + 0.2 * torch.randn(D, generator=gen(i)) for i in (3, 4)]
+    cache = q.kv_cache(20, page, Hkv, D, 0.5, 0.25)
+    table = torch.stack([torch.randperm(10, generator=gen(5)), torch.randperm(10, generator=gen(6)) + 10]).int()
+    ws = q.workspace(q.qlin_attn_kv4_workspace_bytes(cache, B, 40, Hq))
+    past = [(torch.zeros(0, Hkv, D), torch.zeros(0, Hkv, D)) for _ in range(B)]
+    lens = [0, 0]
+    for step, nqs in enumerate(([40, 7], [1, 1], [1, 1], [1, 3], [1, 1])):
+        n = sum(nqs)
+        if n <= 8:
+            hid = synth.activations(n, H, synth.gen(10 + step)).cuda()
+            x = q.qlin_gemv(q.QLIN_Q4_0, qkv_w, W, H, hid)
+        else:
+            x = torch.randn(n, W, generator=gen(20 + step)).cuda()
+        pos = torch.cat([torch.arange(c) + L for c, L in zip(nqs, lens)]).int()
+        seq = torch.tensor([b for b in range(B) for _ in range(nqs[b])])
+        slots = table[seq, (pos // page).long()] * page + pos % page
+        lens = [L + c for L, c in zip(lens, nqs)]
+        cu = torch.tensor([0, nqs[0], n], dtype=torch.int32)
+        qo = q.qlin_kv_append(cache, x, Hq, pos.cuda(), slots.int().cuda(), cs.cuda(), w[0].cuda(), w[1].cuda())
+        o = q.qlin_attn_kv4(cache, qo, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), cu.cuda(), max(nqs), ws=ws)
+        xd = x.cpu().double().view(n, -1, D)
+        k, _ = ref.norm_rope(xd[:, Hq:Hq + Hkv], w[1], 1e-6, cs, pos, D, False)
+        kx = ref.values(*ref.quantize(k.float(), 0.5), 0.5)
+        vx = ref.values(*ref.quantize(xd[:, Hq + Hkv:].float(), 0.25), 0.25)
+        past = [(torch.cat([pk, kx[seq == b]]), torch.cat([pv, vx[seq == b]])) for b, (pk, pv) in enumerate(past)]
+        qh = qo.cpu()
+        check_attn(o, torch.tensor(lens), cu, [qh[seq == b] for b in range(B)], [p[0].double() for p in past],
+                   [p[1].double() for p in past], D, D ** -0.5)
+        if n <= 8:
+            y = q.qlin_gemv(q.QLIN_Q4_0, o_w, H, Hq * D, o.flatten(1))
+            assert y.shape == (n, H) and torch.isfinite(y).all()
+    assert q.qlin_ws_status(ws) == 0
