@@ -16,9 +16,577 @@ struct AttnArgs {
     int64_t ldq, ldo, ldb, total_q;
     int max_pages, B, max_q, Hq, G;
     float scale_log2;  // scale * k_scale * log2(e)
-    int window;
+    int window;        // 0: none; below 2^30
     unsigned* status;
+    int RB, min_tiles;  // few rows: row blocks of a (sequence, head); fewest tiles that another CTA is worth
+    int* tickets;       // in the workspace: kMaxParts, zero between calls
+    float* parts;       // then two parts a CTA: rows x D sums, rows {maximum, sum}
 };
+
+// ------------------------------------------------------------------------------------- few rows, a long axis
+//
+// One persistent launch, one CTA an SM.  The work is a list of tiles (sequence, kv head, row block, 4608 bytes of
+// cache), cut into one equal contiguous range a CTA, so that a batch of any lengths keeps every SM busy to the end.
+// Within a CTA the tiles go round its warps; each warp has a ring of its own, filled by bulk copies of whole groups,
+// and a running maximum, sum and P V of its own.  Where a (sequence, head, row block) ends, the warps' parts are
+// joined in shared memory; where it is shared between CTAs, the last of them to finish joins their parts from the
+// workspace, in the order of the CTAs.
+//
+// A tile is S^T = K q^T, then O^T = V^T P^T, both as m16n8k16: the tokens (then the values of V) fill the 16 rows and
+// up to 8 * NT query rows of one kv head the columns, so that every code is dequantized once (to its exact fp16
+// product of code and scale) whatever the group size.  The order of the inner axis is free as long as both
+// operands share it: for S it is the order in which a lane's 16 (8) bytes of a token's row hold the values, for P V the
+// lanes' tokens are four neighbours, whose codes of one block are 32 contiguous bytes.
+template <int D, int NT>
+struct Dec {
+    static constexpr int kWarps = NT == 1 ? 16 : 8;
+    static constexpr int kTile = D == 128 ? 32 : 64;      // tokens a stage
+    static constexpr int kGroups = kTile / kGroup;
+    static constexpr int kStageBytes = kGroups * group_bytes(D);
+    static constexpr int kStages = NT == 1 ? 3 : 6;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kSteps = D / 16;  // k-steps of S, and 16-row tiles of O^T
+    static constexpr int kPad = D + 8;     // floats a row of a warp's O in its stage buffer
+    static constexpr int kRing = kWarps * kStages * kStageBytes;
+    static constexpr int kFixed = kRing + kWarps * kStages * 16 + kWarps * 8 * 8 + 16;
+    static constexpr int smem(int B) { return kFixed + (B + 1) * 4; }
+};
+constexpr int kMaxParts = 512;  // CTAs of a launch at most: tickets in the workspace
+static_assert(Dec<128, 1>::smem(1024) <= 232448 && Dec<64, 2>::smem(1024) <= 232448, "shared memory");
+static_assert(8 * Dec<128, 1>::kPad * 4 <= Dec<128, 1>::kStageBytes, "a warp's O of 8 rows fits a stage");
+
+// A sequence's queries, context and tiles; bad ones have none.
+struct Seq {
+    int64_t row0;
+    int n, L, tile0, per;
+    bool bad;
+};
+template <int TILE>
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
+    Seq s;
+    s.row0 = __ldg(a.cu + b);
+    s.n = __ldg(a.cu + b + 1) - (int)s.row0;
+    s.L = __ldg(a.lens + b);
+    s.bad = s.n < 0 || s.n > a.max_q || s.row0 < 0 || s.row0 + s.n > a.total_q || s.L < 0 ||
+            (int64_t)s.L > ((int64_t)a.max_pages << a.cache.page_log);
+    s.tile0 = s.per = 0;
+    if (!s.bad && s.n > 0 && s.L > 0) {
+        // the first place that the first query sees
+        const int64_t lo = a.window > 0 ? (int64_t)s.L - s.n + 1 - a.window : 0;
+        s.tile0 = lo > 0 ? (int)(lo / TILE) : 0;
+        s.per = (s.L + TILE - 1) / TILE - s.tile0;
+    }
+    return s;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+// The four f16x2 values of a word's bytes (low half: the byte's low nibble).
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n cvt.rn.f16x2.e2m1x2 %0, b0;\n"
+        " cvt.rn.f16x2.e2m1x2 %1, b1;\n cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// A place in the list of tiles: tile i of (sequence b, head and row block hr).
+struct Cursor {
+    int b, hr, i, per;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel(const AttnArgs a) {
+    using C = Dec<D, NT>;
+    constexpr int W = C::kWarps, S = C::kStages, TILE = C::kTile, NG = C::kGroups, KS = C::kSteps;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRing);
+    uint32_t* bad_groups = reinterpret_cast<uint32_t*>(bars + W * S);
+    float2* red = reinterpret_cast<float2*>(bad_groups + 2 * W * S);  // [warp][8 rows] {m, l}
+    int* flag = reinterpret_cast<int*>(red + W * 8);
+    int* prefix = flag + 4;  // [B + 1] tiles of one (head, row block) before sequence b
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int HR = a.cache.Hkv * a.RB;
+
+    if (lane < S) mbar_init(&bars[warp * S + lane], NG);
+    if (warp == 0) {
+        int run = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            const int b = b0 + lane;
+            int v = 0;
+            if (b < a.B) {
+                const Seq s = seq_of<TILE>(a, b);
+                v = s.per;
+                if (s.bad && blockIdx.x == 0) atomicOr(a.status, kStatusBad);
+            }
+#pragma unroll
+            for (int k = 1; k < 32; k <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, k);
+                if (lane >= k) v += u;
+            }
+            if (b < a.B) prefix[b + 1] = run + v;
+            run += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) prefix[0] = 0;
+    }
+    fence_mbar_init();
+    __syncthreads();
+
+    // queries that see nothing at all: rows of zeros
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        if (prefix[b + 1] > prefix[b]) continue;
+        const Seq s = seq_of<TILE>(a, b);
+        if (s.bad) continue;
+        for (int64_t i = threadIdx.x; i < (int64_t)s.n * a.Hq * D / 8; i += W * 32) {
+            const int64_t r = i / (a.Hq * D / 8), c = i % (a.Hq * D / 8);
+            *reinterpret_cast<uint4*>(a.out + (s.row0 + r) * a.ldo + c * 8) = make_uint4(0, 0, 0, 0);
+        }
+    }
+
+    // this CTA's range of tiles
+    const int64_t T = (int64_t)prefix[a.B] * HR;
+    const int64_t want = (T + a.min_tiles - 1) / a.min_tiles;
+    const int P = (int)(want < gridDim.x ? want : gridDim.x);
+    if ((int)blockIdx.x >= P) return;
+    const int64_t t0 = T * blockIdx.x / P, t1 = T * (blockIdx.x + 1) / P;
+
+    auto locate = [&](int64_t tile) {
+        Cursor c;
+        int lo = 0, hi = a.B - 1;  // the last b with prefix[b] * HR <= tile (it has tiles)
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((int64_t)prefix[mid] * HR <= tile) lo = mid;
+            else hi = mid - 1;
+        }
+        c.b = lo;
+        c.per = prefix[lo + 1] - prefix[lo];
+        const int64_t u = tile - (int64_t)prefix[lo] * HR;
+        c.hr = (int)(u / c.per);
+        c.i = (int)(u - (int64_t)c.hr * c.per);
+        return c;
+    };
+    auto skip = [&](Cursor& c, int n) {  // n tiles on; the end of the list is not reached
+        c.i += n;
+        while (c.i >= c.per) {
+            c.i -= c.per;
+            if (++c.hr == HR) {
+                c.hr = 0;
+                do {
+                    ++c.b;
+                    c.per = prefix[c.b + 1] - prefix[c.b];
+                } while (c.per == 0);
+            }
+        }
+    };
+
+    // this warp's tiles: t0 + warp, t0 + warp + W, ..
+    int mine = t1 - t0 > warp ? (int)((t1 - t0 - warp + W - 1) / W) : 0;
+    Cursor pc = {}, cc = {};
+    if (mine > 0) pc = cc = locate(t0 + warp);
+    int issued = 0;
+    uint8_t* ring = smem + warp * S * C::kStageBytes;
+    auto issue = [&]() {  // lane j copies group j of the next tile
+        const int s = issued % S;
+        if (lane < NG) {
+            const Seq q = seq_of<TILE>(a, pc.b);
+            const int tok = (q.tile0 + pc.i) * TILE + lane * kGroup, h = pc.hr / a.RB;
+            int64_t page = -1;
+            if (tok < q.L) {
+                page = __ldg(a.table + pc.b * a.ldb + (tok >> a.cache.page_log));
+                if (page < 0 || page >= a.cache.n_pages) {
+                    atomicOr(a.status, kStatusBad);
+                    page = -1;
+                }
+            }
+            uint64_t* bar = &bars[warp * S + s];
+            const unsigned ok = __ballot_sync((1u << NG) - 1, page >= 0);
+            if (lane == 0) bad_groups[warp * S + s] = ~ok;
+            mbar_arrive_expect_tx(bar, page >= 0 ? group_bytes(D) : 0);
+            if (page >= 0)
+                bulk_g2s(ring + s * C::kStageBytes + lane * group_bytes(D),
+                         group_ptr<D>(a.cache, page, h, tok & ((1 << a.cache.page_log) - 1)), group_bytes(D), bar);
+        }
+        __syncwarp();
+        ++issued;
+        if (issued < mine) skip(pc, W);
+    };
+    // one stage stays free: the last one read, which holds the warp's O while the warps' parts are joined
+    for (int k = 0; k < S - 1 && k < mine; ++k) issue();
+
+    Cursor seg = locate(t0);
+    int64_t s0 = t0 - seg.i;  // the first tile of this (sequence, head, row block)
+    int done = 0;
+    bool failed = false;
+    for (;;) {
+        const Seq q = seq_of<TILE>(a, seg.b);
+        const int h = seg.hr / a.RB, rb = seg.hr % a.RB;
+        const int rows = min(C::kRows, q.n * a.G - rb * C::kRows);  // may be <= 0
+        const int64_t s1 = s0 + seg.per;
+        // the queries as the columns' operand: column g of lane (g, t) holds values (D / 4) t .. of row g, as fp16
+        // scaled by a power of two that puts the row's largest magnitude in [2^14, 2^15): exact but for
+        // values 2^28 below it
+        uint32_t qf[NT][KS][2];
+        float rs[NT][2], m[NT][2], l[NT][2];
+        int hi[NT][2];
+        float o[KS][NT][4];
+        const bool any = done < mine && cc.b == seg.b && cc.hr == seg.hr;
+        if (any) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int r = nt * 8 + g, rr = rb * C::kRows + r;
+                uint32_t raw[KS * 2];
+                float mx = 0.f;
+                if (r < rows) {
+                    const __nv_bfloat16* p =
+                        a.q + (q.row0 + rr / a.G) * a.ldq + (int64_t)(h * a.G + rr % a.G) * D + t * (D / 4);
+#pragma unroll
+                    for (int k = 0; k < KS / 2; ++k) {
+                        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + k);
+                        raw[4 * k] = u.x, raw[4 * k + 1] = u.y, raw[4 * k + 2] = u.z, raw[4 * k + 3] = u.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < KS * 2; ++k) raw[k] = 0u;
+                }
+#pragma unroll
+                for (int k = 0; k < KS * 2; ++k)
+                    mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(raw[k] << 16)), fabsf(__uint_as_float(raw[k] & 0xffff0000u))));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                // exponent of the largest magnitude, kept where both 2^(14 - e) and 2^(e - 14) are normal numbers
+                const int e = max(min((int)(__float_as_uint(mx) >> 23) - 127, 126), -100);
+                const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+                const float down = a.scale_log2 * __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t w = raw[2 * k + c];
+                        qf[nt][k][c] = pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+                    }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    rs[nt][c] = __shfl_sync(0xffffffffu, down, (2 * t + c) * 4);
+                    const int row = rb * C::kRows + nt * 8 + 2 * t + c;
+                    hi[nt][c] = q.L - q.n + row / a.G;  // the last place that the column's query sees
+                    m[nt][c] = -INFINITY;
+                    l[nt][c] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[i][nt][c] = 0.f;
+        }
+        while (done < mine && cc.b == seg.b && cc.hr == seg.hr) {
+            const int s = done % S;
+            if (!mbar_wait_bounded(&bars[warp * S + s], (done / S) & 1, failed ? 50000000ull : 2000000000ull)) {
+                if (lane == 0) atomicOr(a.status, 1u);
+                failed = true;
+                mine = issued;  // nothing more is copied; what is in flight is waited for
+            }
+            const uint8_t* st = ring + s * C::kStageBytes;
+            const int tok0 = (q.tile0 + cc.i) * TILE;
+            // S^T: rows g and g + 8 of a group's 16 are its tokens ta and ta + 2
+            const int ta = 4 * (g >> 1) + (g & 1);
+            float sc[NG][NT][4];
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                const uint8_t* gp = st + gr * group_bytes(D);
+                uint32_t w0[D / 32], w1[D / 32], f0[D / 64], f1[D / 64];
+                if constexpr (D == 128) {
+                    const uint4 x = lds128(gp + ta * 64 + t * 16), y = lds128(gp + (ta + 2) * 64 + t * 16);
+                    w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
+                    w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
+                    const uint32_t z0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(gp + k_scale_off(D) + ta * 8 + t * 2));
+                    const uint32_t z1 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(gp + k_scale_off(D) + (ta + 2) * 8 + t * 2));
+                    f0[0] = __byte_perm(z0, 0, 0x1010), f0[1] = __byte_perm(z0, 0, 0x3232);
+                    f1[0] = __byte_perm(z1, 0, 0x1010), f1[1] = __byte_perm(z1, 0, 0x3232);
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2*>(gp + ta * 32 + t * 8);
+                    const uint2 y = *reinterpret_cast<const uint2*>(gp + (ta + 2) * 32 + t * 8);
+                    w0[0] = x.x, w0[1] = x.y;
+                    w1[0] = y.x, w1[1] = y.y;
+                    const uint32_t z = e4m3x2_to_f16x2((uint32_t)gp[k_scale_off(D) + ta * 4 + t] |
+                                                       (uint32_t)gp[k_scale_off(D) + (ta + 2) * 4 + t] << 8);
+                    f0[0] = __byte_perm(z, 0, 0x1010), f1[0] = __byte_perm(z, 0, 0x3232);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) sc[gr][nt][c] = 0.f;
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {  // a word of codes: two steps of the inner axis
+                    uint32_t h0[4], h1[4];
+                    e2m1x8(w0[w], h0);
+                    e2m1x8(w1[w], h1);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) h0[c] = hmul2(h0[c], f0[w / 2]), h1[c] = hmul2(h1[c], f1[w / 2]);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t af[4] = {h0[2 * u], h1[2 * u], h0[2 * u + 1], h1[2 * u + 1]};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816(sc[gr][nt], af, qf[nt][2 * w + u][0], qf[nt][2 * w + u][1]);
+                    }
+                }
+            }
+            const uint32_t bad = bad_groups[warp * S + s] & ((1u << NG) - 1);
+            // every row sees all of the tile's tokens, unless the tile reaches past the first row's place or
+            // before the last one's window
+            const bool edge = bad != 0 || tok0 + TILE - 1 > q.L - q.n || (a.window > 0 && tok0 <= q.L - 1 - a.window);
+            float mx[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v = -INFINITY;
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            float x = sc[gr][nt][2 * u + c] * rs[nt][c];
+                            if (edge) {
+                                const int tok = tok0 + gr * kGroup + ta + 2 * u;
+                                const bool sees = tok <= hi[nt][c] && tok < q.L && !((bad >> gr) & 1) &&
+                                                  (a.window == 0 || tok > hi[nt][c] - a.window);
+                                x = sees ? x : -INFINITY;
+                            }
+                            sc[gr][nt][2 * u + c] = x;
+                            v = fmaxf(v, x);
+                        }
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    mx[nt][c] = v;
+                }
+            // The reference that is taken off the scores follows the maximum only when that has grown by 2^8: the
+            // probabilities then reach 2^8, which fp16 holds, and O is rescaled rarely.
+            bool grow = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) grow |= mx[nt][c] > m[nt][c] + 8.f;
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float f[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float mn = fmaxf(m[nt][c], mx[nt][c]);
+                        f[c] = m[nt][c] == -INFINITY ? 0.f : ex2(m[nt][c] - mn);
+                        m[nt][c] = mn;
+                        l[nt][c] *= f[c];
+                    }
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) o[i][nt][c] *= f[c & 1];
+                }
+            }
+            uint32_t pf[NG][NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float ref[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) ref[c] = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) {
+                    float p[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        p[c] = ex2(sc[gr][nt][c] - ref[c & 1]);
+                        l[nt][c & 1] += p[c];
+                    }
+                    // tokens to rows, heads to columns: the transpose is the operand that P V takes
+                    pf[gr][nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
+                    pf[gr][nt][1] = transpose8x8(pack_f16x2(p[2], p[3]));
+                }
+            }
+            // O^T: this lane's tokens of a group are 4 t .. 4 t + 3; row g (g + 8) of tile i is its value 2 i (2 i + 1)
+            // of D / 8 neighbouring values
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                const uint8_t* gp = st + gr * group_bytes(D);
+                constexpr int VW = D / 64;  // words of codes a token
+                const int blk = D == 128 ? g : g >> 1;
+                uint32_t v[4][VW];
+                if constexpr (D == 128) {
+                    const uint4 x = lds128(gp + v_code_off(D) + blk * 128 + t * 32);
+                    const uint4 y = lds128(gp + v_code_off(D) + blk * 128 + t * 32 + 16);
+                    v[0][0] = x.x, v[0][1] = x.y, v[1][0] = x.z, v[1][1] = x.w;
+                    v[2][0] = y.x, v[2][1] = y.y, v[3][0] = y.z, v[3][1] = y.w;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[k][0] = *reinterpret_cast<const uint32_t*>(gp + v_code_off(D) + blk * 128 + t * 32 + k * 8 + (g & 1) * 4);
+                }
+                uint32_t vs = *reinterpret_cast<const uint32_t*>(gp + v_scale_off(D) + blk * 16 + t * 4);
+                if (edge) {  // places behind the end hold anything: scale 0, so that 0 * value is 0
+                    const int left = (bad >> gr) & 1 ? 0 : q.L - (tok0 + gr * kGroup + 4 * t);
+                    vs = left >= 4 ? vs : left <= 0 ? 0u : vs & ((1u << (8 * left)) - 1u);
+                }
+                const uint32_t f01 = e4m3x2_to_f16x2(vs & 0xffffu), f23 = e4m3x2_to_f16x2(vs >> 16);
+#pragma unroll
+                for (int w = 0; w < VW; ++w) {
+                    constexpr uint32_t lo = 0x0f0f0f0fu;
+                    uint32_t x01[4], y01[4], x23[4], y23[4];
+                    e2m1x8((v[0][w] & lo) | ((v[1][w] << 4) & ~lo), x01);
+                    e2m1x8(((v[0][w] >> 4) & lo) | (v[1][w] & ~lo), y01);
+                    e2m1x8((v[2][w] & lo) | ((v[3][w] << 4) & ~lo), x23);
+                    e2m1x8(((v[2][w] >> 4) & lo) | (v[3][w] & ~lo), y23);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t af[4] = {hmul2(x01[i], f01), hmul2(y01[i], f01), hmul2(x23[i], f23), hmul2(y23[i], f23)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816(o[4 * w + i][nt], af, pf[gr][nt][0], pf[gr][nt][1]);
+                    }
+                }
+            }
+            ++done;
+            if (done < mine) skip(cc, W);
+            __syncwarp();
+            if (issued < mine) issue();  // into the stage that was read before this one
+        }
+
+        // join the warps' parts, 8 rows at a time, in the order of the warps
+        const int c0 = (int)(((s0 + 1) * P - 1) / T), c1 = (int)((s1 * P - 1) / T);
+        const bool whole = c0 == c1;
+        float* part = a.parts + (int64_t)(2 * blockIdx.x + ((int)blockIdx.x == c0)) * C::kRows * (D + 2);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float* mo = reinterpret_cast<float*>(ring + ((done + S - 1) % S) * C::kStageBytes);
+            if (any) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v = l[nt][c];
+                    v += __shfl_xor_sync(0xffffffffu, v, 4);
+                    v += __shfl_xor_sync(0xffffffffu, v, 8);
+                    v += __shfl_xor_sync(0xffffffffu, v, 16);
+                    if (g == 0) red[warp * 8 + 2 * t + c] = make_float2(m[nt][c], v);
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {  // the pair of values (KS g + i), its place among 8 (4) turned by g
+                        const int at = KS * g + (i ^ (g & (KS - 1)));
+                        *reinterpret_cast<float2*>(mo + (2 * t + c) * C::kPad + 2 * at) = make_float2(o[i][nt][c], o[i][nt][2 + c]);
+                    }
+                }
+            } else if (lane < 8) {
+                red[warp * 8 + lane] = make_float2(-INFINITY, 0.f);
+            }
+            // where each warp's buffer lies: a warp without a tile of its own is not read
+            if (lane == 0) bad_groups[W * S + warp] = (uint32_t)((done + S - 1) % S);
+            __syncthreads();
+            for (int e = threadIdx.x; e < 8 * D / 2; e += W * 32) {
+                const int r = e / (D / 2), pair = e % (D / 2);
+                if (nt * 8 + r >= rows) break;
+                const int pg = pair / KS, at = KS * pg + ((pair % KS) ^ (pg & (KS - 1)));
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < W; ++w) M = fmaxf(M, red[w * 8 + r].x);
+                float2 acc = make_float2(0.f, 0.f);
+                float sum = 0.f;
+                if (M != -INFINITY) {
+#pragma unroll 4
+                    for (int w = 0; w < W; ++w) {
+                        const float2 ml = red[w * 8 + r];
+                        if (ml.x == -INFINITY) continue;
+                        const float f = ex2(ml.x - M);
+                        const float2 v = *reinterpret_cast<const float2*>(
+                            smem + (w * S + bad_groups[W * S + w]) * C::kStageBytes + (r * C::kPad + 2 * at) * 4);
+                        acc.x += f * v.x, acc.y += f * v.y;
+                        sum += f * ml.y;
+                    }
+                }
+                if (whole) {
+                    const float inv = sum > 0.f ? a.cache.v_scale / sum : 0.f;
+                    const int rr = rb * C::kRows + nt * 8 + r;
+                    *reinterpret_cast<__nv_bfloat162*>(a.out + (q.row0 + rr / a.G) * a.ldo +
+                                                       (int64_t)(h * a.G + rr % a.G) * D + 2 * pair) =
+                        __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+                } else {
+                    __stcg(reinterpret_cast<float2*>(part + (nt * 8 + r) * D + 2 * pair), acc);
+                    if (pair == 0) __stcg(reinterpret_cast<float2*>(part + C::kRows * D + 2 * (nt * 8 + r)), make_float2(M, sum));
+                }
+            }
+            __syncthreads();
+        }
+        if (!whole) {
+            // the last CTA of this (sequence, head, row block) to come here joins the CTAs' parts
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                const int before = atomicAdd(&a.tickets[c0], 1);
+                *flag = before == c1 - c0;
+                if (*flag) a.tickets[c0] = 0;  // everyone has come: zero for the next call
+                __threadfence();
+            }
+            __syncthreads();
+            if (*flag) {
+                const int64_t psz = (int64_t)C::kRows * (D + 2);
+                for (int e = threadIdx.x; e < rows * D / 2; e += W * 32) {
+                    const int r = e / (D / 2), pair = e % (D / 2);
+                    float M = -INFINITY, sum = 0.f;
+                    for (int c = c0; c <= c1; ++c)
+                        M = fmaxf(M, __ldcg(a.parts + (2 * c + (c == c0)) * psz + C::kRows * D + 2 * r));
+                    float2 acc = make_float2(0.f, 0.f);
+                    if (M != -INFINITY) {
+#pragma unroll 4
+                        for (int c = c0; c <= c1; ++c) {
+                            const float* p = a.parts + (2 * c + (c == c0)) * psz;
+                            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + C::kRows * D + 2 * r));
+                            const float2 v = __ldcg(reinterpret_cast<const float2*>(p + r * D + 2 * pair));
+                            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+                            acc.x += f * v.x, acc.y += f * v.y;
+                            sum += f * ml.y;
+                        }
+                    }
+                    const float inv = sum > 0.f ? a.cache.v_scale / sum : 0.f;
+                    const int rr = rb * C::kRows + r;
+                    *reinterpret_cast<__nv_bfloat162*>(a.out + (q.row0 + rr / a.G) * a.ldo +
+                                                       (int64_t)(h * a.G + rr % a.G) * D + 2 * pair) =
+                        __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+                }
+            }
+        }
+        // the joining wrote stages that bulk copies fill next
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (s1 >= t1) break;
+        seg.i = 0;
+        skip(seg, seg.per);
+        s0 = s1;
+    }
+}
+
 
 template <int D>
 __global__ void __launch_bounds__(128) attn_simple_kernel(const AttnArgs a) {
@@ -106,9 +674,41 @@ __global__ void __launch_bounds__(128) attn_simple_kernel(const AttnArgs a) {
 
 using namespace qlin;
 
+static int kv_sm_count() {
+    static int cached[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (cached[dev] == 0) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        cached[dev] = n < kv::kMaxParts ? n : kv::kMaxParts;
+    }
+    return cached[dev];
+}
+
 extern "C" size_t qlin_attn_kv4_ws_bytes(const qlin_kv_cache* c, int B, int max_q, int Hq) {
-    (void)c, (void)B, (void)max_q, (void)Hq;
-    return 256;
+    (void)B;
+    const int rows = max_q * (Hq / c->Hkv) <= 8 ? 8 : 16;
+    return 256 + kv::kMaxParts * 4 + (size_t)2 * kv_sm_count() * rows * (c->D + 2) * 4;
+}
+
+template <int D, int NT>
+static cudaError_t launch_decode(const kv::AttnArgs& a, cudaStream_t s) {
+    using C = kv::Dec<D, NT>;
+    static bool set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64) return cudaErrorInvalidDevice;
+    if (!set[dev]) {
+        e = cudaFuncSetAttribute(kv::attn_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(1024));
+        if (e != cudaSuccess) return e;
+        set[dev] = true;
+    }
+    const int sms = kv_sm_count();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    kv::attn_decode_kernel<D, NT><<<sms, C::kWarps * 32, C::smem(a.B), s>>>(a);
+    return cudaGetLastError();
 }
 
 extern "C" cudaError_t qlin_launch_attn_kv4(const qlin_kv_cache* c, const void* q, int64_t ldq, const int32_t* table,
@@ -121,8 +721,17 @@ extern "C" cudaError_t qlin_launch_attn_kv4(const qlin_kv_cache* c, const void* 
     a.table = table, a.lens = lens, a.cu = cu, a.ldq = ldq, a.ldo = ldo, a.ldb = ldb, a.total_q = total_q;
     a.max_pages = max_pages, a.B = B, a.max_q = max_q, a.Hq = Hq, a.G = Hq / c->Hkv;
     a.scale_log2 = scale * c->k_scale * 1.4426950408889634f;
-    a.window = window;
+    a.window = window < (1 << 30) ? window : 0;  // no context is longer
     a.status = (unsigned*)ws;
+    a.tickets = (int*)((uint8_t*)ws + 256);
+    a.parts = (float*)((uint8_t*)ws + 256 + kv::kMaxParts * 4);
+    a.min_tiles = 8;
+    const int64_t rows = (int64_t)max_q * a.G;
+    if (rows <= 64) {
+        a.RB = rows <= 8 ? 1 : (int)((rows + 15) / 16);
+        if (c->D == 128) return rows <= 8 ? launch_decode<128, 1>(a, s) : launch_decode<128, 2>(a, s);
+        return rows <= 8 ? launch_decode<64, 1>(a, s) : launch_decode<64, 2>(a, s);
+    }
     const dim3 grid((unsigned)max_q, (unsigned)((Hq + 3) / 4), (unsigned)B);
     if (c->D == 128)
         kv::attn_simple_kernel<128><<<grid, 128, 0, s>>>(a);
