@@ -3,6 +3,8 @@
 //
 // A warp per (query, query head): 32 tokens at a time, a token a lane, with the running maximum and sum of the
 // softmax; the probabilities then go round the warp while each lane sums its D / 32 values of V.
+#include <cuda/std/type_traits>
+
 #include "kv_cache.cuh"
 
 namespace qlin {
@@ -210,16 +212,21 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
     // this warp's tiles: t0 + warp, t0 + warp + W, ..
     int mine = t1 - t0 > warp ? (int)((t1 - t0 - warp + W - 1) / W) : 0;
     Cursor pc = {}, cc = {};
+    int issued = 0, pb = -1, pL = 0, ptok = 0;  // pb: the sequence whose length and first place pL and ptok are
     if (mine > 0) pc = cc = locate(t0 + warp);
-    int issued = 0;
     uint8_t* ring = smem + warp * S * C::kStageBytes;
+    const unsigned heads_groups = (unsigned)a.cache.Hkv << (a.cache.page_log - 4);
     auto issue = [&]() {  // lane j copies group j of the next tile
         const int s = issued % S;
-        if (lane < NG) {
+        if (pc.b != pb) {
             const Seq q = seq_of<TILE>(a, pc.b);
-            const int tok = (q.tile0 + pc.i) * TILE + lane * kGroup, h = pc.hr / a.RB;
+            pb = pc.b, pL = q.L, ptok = q.tile0 * TILE;
+        }
+        if (lane < NG) {
+            const int tok = ptok + pc.i * TILE + lane * kGroup;
+            const int h = a.RB == 1 ? pc.hr : pc.hr / a.RB;
             int64_t page = -1;
-            if (tok < q.L) {
+            if (tok < pL) {
                 page = __ldg(a.table + pc.b * a.ldb + (tok >> a.cache.page_log));
                 if (page < 0 || page >= a.cache.n_pages) {
                     atomicOr(a.status, kStatusBad);
@@ -228,11 +235,14 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
             }
             uint64_t* bar = &bars[warp * S + s];
             const unsigned ok = __ballot_sync((1u << NG) - 1, page >= 0);
-            if (lane == 0) bad_groups[warp * S + s] = ~ok;
+            if (lane == 0) bad_groups[warp * S + s] = ~ok & ((1u << NG) - 1);
             mbar_arrive_expect_tx(bar, page >= 0 ? group_bytes(D) : 0);
-            if (page >= 0)
+            if (page >= 0) {
+                const unsigned in = ((unsigned)h << (a.cache.page_log - 4)) +
+                                    ((tok & ((1 << a.cache.page_log) - 1)) >> 4);  // group within the page
                 bulk_g2s(ring + s * C::kStageBytes + lane * group_bytes(D),
-                         group_ptr<D>(a.cache, page, h, tok & ((1 << a.cache.page_log) - 1)), group_bytes(D), bar);
+                         a.cache.data + ((uint64_t)(unsigned)page * heads_groups + in) * group_bytes(D), group_bytes(D), bar);
+            }
         }
         __syncwarp();
         ++issued;
@@ -251,8 +261,8 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         const int rows = min(C::kRows, q.n * a.G - rb * C::kRows);  // may be <= 0
         const int64_t s1 = s0 + seg.per;
         // the queries as the columns' operand: column g of lane (g, t) holds values (D / 4) t .. of row g, as fp16
-        // scaled by a power of two that puts the row's largest magnitude in [2^14, 2^15): exact but for
-        // values 2^28 below it
+        // scaled by a power of two (with the sign of the scale) that puts the row's largest magnitude in
+        // [2^14, 2^15): exact but for values 2^28 below it.  rs takes the scores to the exponents of 2.
         uint32_t qf[NT][KS][2];
         float rs[NT][2], m[NT][2], l[NT][2];
         int hi[NT][2];
@@ -283,8 +293,8 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 // exponent of the largest magnitude, kept where both 2^(14 - e) and 2^(e - 14) are normal numbers
                 const int e = max(min((int)(__float_as_uint(mx) >> 23) - 127, 126), -100);
-                const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
-                const float down = a.scale_log2 * __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+                const float up = copysignf(__uint_as_float((uint32_t)(14 - e + 127) << 23), a.scale_log2);
+                const float down = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(e - 14 + 127) << 23);
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -317,161 +327,172 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
             }
             const uint8_t* st = ring + s * C::kStageBytes;
             const int tok0 = (q.tile0 + cc.i) * TILE;
-            // S^T: rows g and g + 8 of a group's 16 are its tokens ta and ta + 2
-            const int ta = 4 * (g >> 1) + (g & 1);
-            float sc[NG][NT][4];
+            const uint32_t bad = bad_groups[warp * S + s];
+            // every row sees all of the tile's tokens, unless the tile reaches past the first row's place or
+            // before the last one's window: the common form has no masks at all
+            auto step = [&](auto masked) {
+                constexpr bool edge = decltype(masked)::value;
+                // S^T: rows g and g + 8 of a group's 16 are its tokens ta and ta + 2
+                const int ta = 4 * (g >> 1) + (g & 1);
+                float sc[NG][NT][4];
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-                const uint8_t* gp = st + gr * group_bytes(D);
-                uint32_t w0[D / 32], w1[D / 32], f0[D / 64], f1[D / 64];
-                if constexpr (D == 128) {
-                    const uint4 x = lds128(gp + ta * 64 + t * 16), y = lds128(gp + (ta + 2) * 64 + t * 16);
-                    w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
-                    w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
-                    const uint32_t z0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(gp + k_scale_off(D) + ta * 8 + t * 2));
-                    const uint32_t z1 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(gp + k_scale_off(D) + (ta + 2) * 8 + t * 2));
-                    f0[0] = __byte_perm(z0, 0, 0x1010), f0[1] = __byte_perm(z0, 0, 0x3232);
-                    f1[0] = __byte_perm(z1, 0, 0x1010), f1[1] = __byte_perm(z1, 0, 0x3232);
-                } else {
-                    const uint2 x = *reinterpret_cast<const uint2*>(gp + ta * 32 + t * 8);
-                    const uint2 y = *reinterpret_cast<const uint2*>(gp + (ta + 2) * 32 + t * 8);
-                    w0[0] = x.x, w0[1] = x.y;
-                    w1[0] = y.x, w1[1] = y.y;
-                    const uint32_t z = e4m3x2_to_f16x2((uint32_t)gp[k_scale_off(D) + ta * 4 + t] |
-                                                       (uint32_t)gp[k_scale_off(D) + (ta + 2) * 4 + t] << 8);
-                    f0[0] = __byte_perm(z, 0, 0x1010), f1[0] = __byte_perm(z, 0, 0x3232);
-                }
+                for (int gr = 0; gr < NG; ++gr) {
+                    const uint8_t* gp = st + gr * group_bytes(D);
+                    uint32_t w0[D / 32], w1[D / 32], f0[D / 64], f1[D / 64];
+                    if constexpr (D == 128) {
+                        const uint4 x = lds128(gp + ta * 64 + t * 16), y = lds128(gp + (ta + 2) * 64 + t * 16);
+                        w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
+                        w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
+                        const uint32_t z0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(gp + k_scale_off(D) + ta * 8 + t * 2));
+                        const uint32_t z1 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(gp + k_scale_off(D) + (ta + 2) * 8 + t * 2));
+                        f0[0] = __byte_perm(z0, 0, 0x1010), f0[1] = __byte_perm(z0, 0, 0x3232);
+                        f1[0] = __byte_perm(z1, 0, 0x1010), f1[1] = __byte_perm(z1, 0, 0x3232);
+                    } else {
+                        const uint2 x = *reinterpret_cast<const uint2*>(gp + ta * 32 + t * 8);
+                        const uint2 y = *reinterpret_cast<const uint2*>(gp + (ta + 2) * 32 + t * 8);
+                        w0[0] = x.x, w0[1] = x.y;
+                        w1[0] = y.x, w1[1] = y.y;
+                        const uint32_t z = e4m3x2_to_f16x2((uint32_t)gp[k_scale_off(D) + ta * 4 + t] |
+                                                           (uint32_t)gp[k_scale_off(D) + (ta + 2) * 4 + t] << 8);
+                        f0[0] = __byte_perm(z, 0, 0x1010), f1[0] = __byte_perm(z, 0, 0x3232);
+                    }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) sc[gr][nt][c] = 0.f;
+                        for (int c = 0; c < 4; ++c) sc[gr][nt][c] = 0.f;
 #pragma unroll
-                for (int w = 0; w < D / 32; ++w) {  // a word of codes: two steps of the inner axis
-                    uint32_t h0[4], h1[4];
-                    e2m1x8(w0[w], h0);
-                    e2m1x8(w1[w], h1);
+                    for (int w = 0; w < D / 32; ++w) {  // a word of codes: two steps of the inner axis
+                        uint32_t h0[4], h1[4];
+                        e2m1x8(w0[w], h0);
+                        e2m1x8(w1[w], h1);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) h0[c] = hmul2(h0[c], f0[w / 2]), h1[c] = hmul2(h1[c], f1[w / 2]);
+                        for (int c = 0; c < 4; ++c) h0[c] = hmul2(h0[c], f0[w / 2]), h1[c] = hmul2(h1[c], f1[w / 2]);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t af[4] = {h0[2 * u], h1[2 * u], h0[2 * u + 1], h1[2 * u + 1]};
+                        for (int u = 0; u < 2; ++u) {
+                            const uint32_t af[4] = {h0[2 * u], h1[2 * u], h0[2 * u + 1], h1[2 * u + 1]};
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816(sc[gr][nt], af, qf[nt][2 * w + u][0], qf[nt][2 * w + u][1]);
+                            for (int nt = 0; nt < NT; ++nt) mma16816(sc[gr][nt], af, qf[nt][2 * w + u][0], qf[nt][2 * w + u][1]);
+                        }
                     }
                 }
-            }
-            const uint32_t bad = bad_groups[warp * S + s] & ((1u << NG) - 1);
-            // every row sees all of the tile's tokens, unless the tile reaches past the first row's place or
-            // before the last one's window
-            const bool edge = bad != 0 || tok0 + TILE - 1 > q.L - q.n || (a.window > 0 && tok0 <= q.L - 1 - a.window);
-            float mx[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float v = -INFINITY;
+                if constexpr (edge) {
 #pragma unroll
                     for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            float x = sc[gr][nt][2 * u + c] * rs[nt][c];
-                            if (edge) {
-                                const int tok = tok0 + gr * kGroup + ta + 2 * u;
-                                const bool sees = tok <= hi[nt][c] && tok < q.L && !((bad >> gr) & 1) &&
-                                                  (a.window == 0 || tok > hi[nt][c] - a.window);
-                                x = sees ? x : -INFINITY;
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const int tok = tok0 + gr * kGroup + ta + (c & 2);
+                                const bool sees = tok <= hi[nt][c & 1] && tok < q.L && !((bad >> gr) & 1) &&
+                                                  (a.window == 0 || tok > hi[nt][c & 1] - a.window);
+                                sc[gr][nt][c] = sees ? sc[gr][nt][c] : -INFINITY;
                             }
-                            sc[gr][nt][2 * u + c] = x;
-                            v = fmaxf(v, x);
-                        }
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    mx[nt][c] = v;
                 }
-            // The reference that is taken off the scores follows the maximum only when that has grown by 2^8: the
-            // probabilities then reach 2^8, which fp16 holds, and O is rescaled rarely.
-            bool grow = false;
+                float mx[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) grow |= mx[nt][c] > m[nt][c] + 8.f;
-            if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float f[2];
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float mn = fmaxf(m[nt][c], mx[nt][c]);
-                        f[c] = m[nt][c] == -INFINITY ? 0.f : ex2(m[nt][c] - mn);
-                        m[nt][c] = mn;
-                        l[nt][c] *= f[c];
+                        float v = -INFINITY;
+#pragma unroll
+                        for (int gr = 0; gr < NG; ++gr) v = fmaxf(v, fmaxf(sc[gr][nt][c], sc[gr][nt][2 + c]));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                        mx[nt][c] = v == -INFINITY ? v : __fmul_rn(v, rs[nt][c]);
                     }
+                // The reference that is taken off the scores follows the maximum only when that has grown by 2^8: the
+                // probabilities then reach 2^8, which fp16 holds, and O is rescaled rarely.
+                bool grow = false;
 #pragma unroll
-                    for (int i = 0; i < KS; ++i)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) o[i][nt][c] *= f[c & 1];
+                    for (int c = 0; c < 2; ++c) grow |= mx[nt][c] > m[nt][c] + 8.f;
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float f[2];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float mn = fmaxf(m[nt][c], mx[nt][c]);
+                            f[c] = m[nt][c] == -INFINITY ? 0.f : ex2(m[nt][c] - mn);
+                            m[nt][c] = mn;
+                            l[nt][c] *= f[c];
+                        }
+#pragma unroll
+                        for (int i = 0; i < KS; ++i)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) o[i][nt][c] *= f[c & 1];
+                    }
                 }
-            }
-            uint32_t pf[NG][NT][2];
+                uint32_t pf[NG][NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float ref[2];
+                for (int nt = 0; nt < NT; ++nt) {
+                    float ref[2];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) ref[c] = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
+                    for (int c = 0; c < 2; ++c) ref[c] = m[nt][c] == -INFINITY ? 0.f : -m[nt][c];
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr) {
+                        float p[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)  // two roundings as in mx: the largest score's exponent is then 0, not a remainder
+                            p[c] = ex2(__fadd_rn(__fmul_rn(sc[gr][nt][c], rs[nt][c & 1]), ref[c & 1]));
+                        if constexpr (edge) {  // also where rs is 0
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) p[c] = sc[gr][nt][c] == -INFINITY ? 0.f : p[c];
+                        }
+                        l[nt][0] += p[0] + p[2];
+                        l[nt][1] += p[1] + p[3];
+                        // tokens to rows, heads to columns: the transpose is the operand that P V takes
+                        pf[gr][nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
+                        pf[gr][nt][1] = transpose8x8(pack_f16x2(p[2], p[3]));
+                    }
+                }
+                // O^T: this lane's tokens of a group are 4 t .. 4 t + 3; row g (g + 8) of tile i is its value 2 i (2 i + 1)
+                // of D / 8 neighbouring values
 #pragma unroll
                 for (int gr = 0; gr < NG; ++gr) {
-                    float p[4];
+                    const uint8_t* gp = st + gr * group_bytes(D);
+                    constexpr int VW = D / 64;  // words of codes a token
+                    const int blk = D == 128 ? g : g >> 1;
+                    uint32_t v[4][VW];
+                    if constexpr (D == 128) {
+                        const uint4 x = lds128(gp + v_code_off(D) + blk * 128 + t * 32);
+                        const uint4 y = lds128(gp + v_code_off(D) + blk * 128 + t * 32 + 16);
+                        v[0][0] = x.x, v[0][1] = x.y, v[1][0] = x.z, v[1][1] = x.w;
+                        v[2][0] = y.x, v[2][1] = y.y, v[3][0] = y.z, v[3][1] = y.w;
+                    } else {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        p[c] = ex2(sc[gr][nt][c] - ref[c & 1]);
-                        l[nt][c & 1] += p[c];
+                        for (int k = 0; k < 4; ++k)
+                            v[k][0] = *reinterpret_cast<const uint32_t*>(gp + v_code_off(D) + blk * 128 + t * 32 + k * 8 + (g & 1) * 4);
                     }
-                    // tokens to rows, heads to columns: the transpose is the operand that P V takes
-                    pf[gr][nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
-                    pf[gr][nt][1] = transpose8x8(pack_f16x2(p[2], p[3]));
-                }
-            }
-            // O^T: this lane's tokens of a group are 4 t .. 4 t + 3; row g (g + 8) of tile i is its value 2 i (2 i + 1)
-            // of D / 8 neighbouring values
+                    uint32_t vs = *reinterpret_cast<const uint32_t*>(gp + v_scale_off(D) + blk * 16 + t * 4);
+                    if constexpr (edge) {  // places behind the end hold anything: scale 0, so that 0 * value is 0
+                        const int left = (bad >> gr) & 1 ? 0 : q.L - (tok0 + gr * kGroup + 4 * t);
+                        vs = left >= 4 ? vs : left <= 0 ? 0u : vs & ((1u << (8 * left)) - 1u);
+                    }
+                    const uint32_t f01 = e4m3x2_to_f16x2(vs & 0xffffu), f23 = e4m3x2_to_f16x2(vs >> 16);
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-                const uint8_t* gp = st + gr * group_bytes(D);
-                constexpr int VW = D / 64;  // words of codes a token
-                const int blk = D == 128 ? g : g >> 1;
-                uint32_t v[4][VW];
-                if constexpr (D == 128) {
-                    const uint4 x = lds128(gp + v_code_off(D) + blk * 128 + t * 32);
-                    const uint4 y = lds128(gp + v_code_off(D) + blk * 128 + t * 32 + 16);
-                    v[0][0] = x.x, v[0][1] = x.y, v[1][0] = x.z, v[1][1] = x.w;
-                    v[2][0] = y.x, v[2][1] = y.y, v[3][0] = y.z, v[3][1] = y.w;
-                } else {
+                    for (int w = 0; w < VW; ++w) {
+                        constexpr uint32_t lo = 0x0f0f0f0fu;
+                        uint32_t x01[4], y01[4], x23[4], y23[4];
+                        e2m1x8((v[0][w] & lo) | ((v[1][w] << 4) & ~lo), x01);
+                        e2m1x8(((v[0][w] >> 4) & lo) | (v[1][w] & ~lo), y01);
+                        e2m1x8((v[2][w] & lo) | ((v[3][w] << 4) & ~lo), x23);
+                        e2m1x8(((v[2][w] >> 4) & lo) | (v[3][w] & ~lo), y23);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        v[k][0] = *reinterpret_cast<const uint32_t*>(gp + v_code_off(D) + blk * 128 + t * 32 + k * 8 + (g & 1) * 4);
-                }
-                uint32_t vs = *reinterpret_cast<const uint32_t*>(gp + v_scale_off(D) + blk * 16 + t * 4);
-                if (edge) {  // places behind the end hold anything: scale 0, so that 0 * value is 0
-                    const int left = (bad >> gr) & 1 ? 0 : q.L - (tok0 + gr * kGroup + 4 * t);
-                    vs = left >= 4 ? vs : left <= 0 ? 0u : vs & ((1u << (8 * left)) - 1u);
-                }
-                const uint32_t f01 = e4m3x2_to_f16x2(vs & 0xffffu), f23 = e4m3x2_to_f16x2(vs >> 16);
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t af[4] = {hmul2(x01[i], f01), hmul2(y01[i], f01), hmul2(x23[i], f23), hmul2(y23[i], f23)};
 #pragma unroll
-                for (int w = 0; w < VW; ++w) {
-                    constexpr uint32_t lo = 0x0f0f0f0fu;
-                    uint32_t x01[4], y01[4], x23[4], y23[4];
-                    e2m1x8((v[0][w] & lo) | ((v[1][w] << 4) & ~lo), x01);
-                    e2m1x8(((v[0][w] >> 4) & lo) | (v[1][w] & ~lo), y01);
-                    e2m1x8((v[2][w] & lo) | ((v[3][w] << 4) & ~lo), x23);
-                    e2m1x8(((v[2][w] >> 4) & lo) | (v[3][w] & ~lo), y23);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t af[4] = {hmul2(x01[i], f01), hmul2(y01[i], f01), hmul2(x23[i], f23), hmul2(y23[i], f23)};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816(o[4 * w + i][nt], af, pf[gr][nt][0], pf[gr][nt][1]);
+                            for (int nt = 0; nt < NT; ++nt) mma16816(o[4 * w + i][nt], af, pf[gr][nt][0], pf[gr][nt][1]);
+                        }
                     }
                 }
-            }
+            };
+            if (bad != 0 || tok0 + TILE - 1 > q.L - q.n || (a.window > 0 && tok0 <= q.L - 1 - a.window))
+                step(cuda::std::true_type());
+            else
+                step(cuda::std::false_type());
             ++done;
             if (done < mine) skip(cc, W);
             __syncwarp();
