@@ -34,6 +34,7 @@ qlin_status_t check_geometry(int64_t n_pages, int page, int Hkv, int D) {
     if (n_pages < 1 || Hkv < 1 || Hkv > kMaxHeads || D < 1) return QLIN_ERR_INVALID_ARG;
     if (page != 16 && page != 32 && page != 64 && page != 128 && page != 256) return QLIN_ERR_INVALID_ARG;
     if (n_pages > (((int64_t)1 << 31) - 1) / page) return QLIN_ERR_INVALID_ARG;
+    if (n_pages * (page / 16) * Hkv >= ((int64_t)1 << 32) - 1) return QLIN_ERR_UNSUPPORTED;  // groups are numbered in 32 bits
     return D == 64 || D == 128 ? QLIN_OK : QLIN_ERR_UNSUPPORTED;
 }
 

@@ -50,11 +50,13 @@ struct Dec {
     static constexpr int kSteps = D / 16;  // k-steps of S, and 16-row tiles of O^T
     static constexpr int kPad = D + 8;     // floats a row of a warp's O in its stage buffer
     static constexpr int kRing = kWarps * kStages * kStageBytes;
-    static constexpr int kFixed = kRing + kWarps * kStages * 16 + kWarps * 8 * 8 + 16;
-    static constexpr int smem(int B) { return kFixed + (B + 1) * 4; }
+    static constexpr int kBatch = 64 / kGroups;  // tiles whose sources a warp looks up at once
+    static constexpr int kFixed = kRing + kWarps * kStages * 16 + kWarps * 8 * 8 + kWarps * 64 * 4 + 16;
+    static constexpr int smem(int B) { return kFixed + (2 * B + 1) * 4; }
 };
 constexpr int kMaxParts = 512;  // CTAs of a launch at most: tickets in the workspace
-static_assert(Dec<128, 1>::smem(1024) <= 232448 && Dec<64, 2>::smem(1024) <= 232448, "shared memory");
+constexpr int kMaxDecSeqs = 512;  // sequences of a launch
+static_assert(Dec<128, 1>::smem(kMaxDecSeqs) <= 232448 && Dec<64, 2>::smem(kMaxDecSeqs) <= 232448, "shared memory");
 static_assert(8 * Dec<128, 1>::kPad * 4 <= Dec<128, 1>::kStageBytes, "a warp's O of 8 rows fits a stage");
 
 // A sequence's queries, context and tiles; bad ones have none.
@@ -133,8 +135,10 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRing);
     uint32_t* bad_groups = reinterpret_cast<uint32_t*>(bars + W * S);
     float2* red = reinterpret_cast<float2*>(bad_groups + 2 * W * S);  // [warp][8 rows] {m, l}
-    int* flag = reinterpret_cast<int*>(red + W * 8);
+    uint32_t* source = reinterpret_cast<uint32_t*>(red + W * 8);  // [warp][64] the cache's groups that its next tiles are
+    int* flag = reinterpret_cast<int*>(source + W * 64);
     int* prefix = flag + 4;  // [B + 1] tiles of one (head, row block) before sequence b
+    int* length = prefix + a.B + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int HR = a.cache.Hkv * a.RB;
 
@@ -147,6 +151,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
             if (b < a.B) {
                 const Seq s = seq_of<TILE>(a, b);
                 v = s.per;
+                length[b] = s.L;
                 if (s.bad && blockIdx.x == 0) atomicOr(a.status, kStatusBad);
             }
 #pragma unroll
@@ -211,47 +216,50 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
 
     // this warp's tiles: t0 + warp, t0 + warp + W, ..
     int mine = t1 - t0 > warp ? (int)((t1 - t0 - warp + W - 1) / W) : 0;
-    Cursor pc = {}, cc = {};
-    int issued = 0, pb = -1, pL = 0, ptok = 0;  // pb: the sequence whose length and first place pL and ptok are
-    if (mine > 0) pc = cc = locate(t0 + warp);
+    int issued = 0;
     uint8_t* ring = smem + warp * S * C::kStageBytes;
     const unsigned heads_groups = (unsigned)a.cache.Hkv << (a.cache.page_log - 4);
     auto issue = [&]() {  // lane j copies group j of the next tile
-        const int s = issued % S;
-        if (pc.b != pb) {
-            const Seq q = seq_of<TILE>(a, pc.b);
-            pb = pc.b, pL = q.L, ptok = q.tile0 * TILE;
+        const int s = issued % S, e = issued % C::kBatch;
+        if (e == 0) {
+            // where the next kBatch tiles lie, a group a lane: the searches and the page table's latency once for all
+#pragma unroll
+            for (int k = lane; k < 64; k += 32) {
+                uint32_t src = 0xffffffffu;  // behind the end, or a bad page: not copied, and masked
+                if (issued + k / NG < mine) {
+                    const Cursor c = locate(t0 + warp + (int64_t)(issued + k / NG) * W);
+                    const int first = a.window > 0 ? seq_of<TILE>(a, c.b).tile0 : 0;
+                    const int tok = (first + c.i) * TILE + (k % NG) * kGroup;
+                    if (tok < length[c.b]) {
+                        const int page = __ldg(a.table + c.b * a.ldb + (tok >> a.cache.page_log));
+                        if (page >= 0 && page < a.cache.n_pages)
+                            src = (unsigned)page * heads_groups + ((unsigned)(c.hr / a.RB) << (a.cache.page_log - 4)) +
+                                  ((tok & ((1 << a.cache.page_log) - 1)) >> 4);
+                        else
+                            atomicOr(a.status, kStatusBad);
+                    }
+                }
+                source[warp * 64 + k] = src;
+            }
+            __syncwarp();
         }
         if (lane < NG) {
-            const int tok = ptok + pc.i * TILE + lane * kGroup;
-            const int h = a.RB == 1 ? pc.hr : pc.hr / a.RB;
-            int64_t page = -1;
-            if (tok < pL) {
-                page = __ldg(a.table + pc.b * a.ldb + (tok >> a.cache.page_log));
-                if (page < 0 || page >= a.cache.n_pages) {
-                    atomicOr(a.status, kStatusBad);
-                    page = -1;
-                }
-            }
+            const uint32_t src = source[warp * 64 + e * NG + lane];
             uint64_t* bar = &bars[warp * S + s];
-            const unsigned ok = __ballot_sync((1u << NG) - 1, page >= 0);
+            const unsigned ok = __ballot_sync((1u << NG) - 1, src != 0xffffffffu);
             if (lane == 0) bad_groups[warp * S + s] = ~ok & ((1u << NG) - 1);
-            mbar_arrive_expect_tx(bar, page >= 0 ? group_bytes(D) : 0);
-            if (page >= 0) {
-                const unsigned in = ((unsigned)h << (a.cache.page_log - 4)) +
-                                    ((tok & ((1 << a.cache.page_log) - 1)) >> 4);  // group within the page
-                bulk_g2s(ring + s * C::kStageBytes + lane * group_bytes(D),
-                         a.cache.data + ((uint64_t)(unsigned)page * heads_groups + in) * group_bytes(D), group_bytes(D), bar);
-            }
+            mbar_arrive_expect_tx(bar, src != 0xffffffffu ? group_bytes(D) : 0);
+            if (src != 0xffffffffu)
+                bulk_g2s(ring + s * C::kStageBytes + lane * group_bytes(D), a.cache.data + (uint64_t)src * group_bytes(D),
+                         group_bytes(D), bar);
         }
         __syncwarp();
         ++issued;
-        if (issued < mine) skip(pc, W);
     };
     // one stage stays free: the last one read, which holds the warp's O while the warps' parts are joined
     for (int k = 0; k < S - 1 && k < mine; ++k) issue();
 
-    Cursor seg = locate(t0);
+    Cursor seg = locate(t0), cc = locate(mine > 0 ? t0 + warp : t0);
     int64_t s0 = t0 - seg.i;  // the first tile of this (sequence, head, row block)
     int done = 0;
     bool failed = false;
@@ -533,19 +541,18 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                 float M = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < W; ++w) M = fmaxf(M, red[w * 8 + r].x);
+                const float top = M == -INFINITY ? 0.f : M;
                 float2 acc = make_float2(0.f, 0.f);
                 float sum = 0.f;
-                if (M != -INFINITY) {
-#pragma unroll 4
-                    for (int w = 0; w < W; ++w) {
-                        const float2 ml = red[w * 8 + r];
-                        if (ml.x == -INFINITY) continue;
-                        const float f = ex2(ml.x - M);
-                        const float2 v = *reinterpret_cast<const float2*>(
-                            smem + (w * S + bad_groups[W * S + w]) * C::kStageBytes + (r * C::kPad + 2 * at) * 4);
-                        acc.x += f * v.x, acc.y += f * v.y;
-                        sum += f * ml.y;
-                    }
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const float2 ml = red[w * 8 + r];
+                    float2 v = *reinterpret_cast<const float2*>(
+                        smem + (w * S + bad_groups[W * S + w]) * C::kStageBytes + (r * C::kPad + 2 * at) * 4);
+                    const float f = ex2(ml.x - top);
+                    if (f == 0.f) v = make_float2(0.f, 0.f);  // also a buffer that holds something else
+                    acc.x += f * v.x, acc.y += f * v.y;
+                    sum += f * ml.y;
                 }
                 if (whole) {
                     const float inv = sum > 0.f ? a.cache.v_scale / sum : 0.f;
@@ -714,7 +721,7 @@ extern "C" size_t qlin_attn_kv4_ws_bytes(const qlin_kv_cache* c, int B, int max_
 }
 
 template <int D, int NT>
-static cudaError_t launch_decode(const kv::AttnArgs& a, cudaStream_t s) {
+static cudaError_t launch_decode(kv::AttnArgs a, cudaStream_t s) {
     using C = kv::Dec<D, NT>;
     static bool set[64] = {};
     int dev = 0;
@@ -722,14 +729,20 @@ static cudaError_t launch_decode(const kv::AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev >= 64) return cudaErrorInvalidDevice;
     if (!set[dev]) {
-        e = cudaFuncSetAttribute(kv::attn_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(1024));
+        e = cudaFuncSetAttribute(kv::attn_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::smem(kv::kMaxDecSeqs));
         if (e != cudaSuccess) return e;
         set[dev] = true;
     }
     const int sms = kv_sm_count();
     if (sms < 1) return cudaErrorInvalidDevice;
-    kv::attn_decode_kernel<D, NT><<<sms, C::kWarps * 32, C::smem(a.B), s>>>(a);
-    return cudaGetLastError();
+    for (int left = a.B; left > 0; left -= kv::kMaxDecSeqs) {
+        a.B = left < kv::kMaxDecSeqs ? left : kv::kMaxDecSeqs;
+        kv::attn_decode_kernel<D, NT><<<sms, C::kWarps * 32, C::smem(a.B), s>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        a.table += a.B * a.ldb, a.lens += a.B, a.cu += a.B;
+    }
+    return cudaSuccess;
 }
 
 extern "C" cudaError_t qlin_launch_attn_kv4(const qlin_kv_cache* c, const void* q, int64_t ldq, const int32_t* table,

@@ -400,7 +400,8 @@ qlin_status_t qlin_dequant_debug(qlin_format_t fmt, const void* packed, int64_t 
  * s / page. */
 typedef struct qlin_kv_cache {
     void* data;             /* qlin_kv_cache_bytes(n_pages, page, Hkv, D) bytes, 256-byte aligned     */
-    int64_t n_pages;        /* n_pages * page < 2^31                                                  */
+    int64_t n_pages;        /* n_pages * page < 2^31; n_pages * page / 16 * Hkv < 2^32 - 1 (else
+                               QLIN_ERR_UNSUPPORTED)                                                  */
     int32_t page;           /* tokens a page: 16, 32, 64, 128 or 256                                  */
     int32_t Hkv;            /* key / value heads, 1 .. 1024                                           */
     int32_t D;              /* values a head: 64 or 128 (else QLIN_ERR_UNSUPPORTED)                   */
