@@ -45,24 +45,33 @@ struct Dec {
     static constexpr int kTile = D == 128 ? 32 : 64;      // tokens a stage
     static constexpr int kGroups = kTile / kGroup;
     static constexpr int kStageBytes = kGroups * group_bytes(D);
-    static constexpr int kStages = NT == 1 ? 3 : 6;
+    static constexpr int kStages = NT == 1 ? 3 : 5;
     static constexpr int kRows = 8 * NT;
     static constexpr int kSteps = D / 16;  // k-steps of S, and 16-row tiles of O^T
     static constexpr int kPad = D + 8;     // floats a row of a warp's O in its stage buffer
     static constexpr int kRing = kWarps * kStages * kStageBytes;
-    static constexpr int kBatch = 64 / kGroups;  // tiles whose sources a warp looks up at once
-    static constexpr int kFixed = kRing + kWarps * kStages * 16 + kWarps * 8 * 8 + kWarps * 64 * 4 + 16;
-    static constexpr int smem(int B) { return kFixed + (2 * B + 1) * 4; }
+    static constexpr int kBatch = 32 / kGroups;  // tiles whose sources a warp looks up at once
+    static constexpr int kQBytes = kRows * (D * 2 + 4);  // a segment's queries as fp16, and their scales
+    static constexpr int kFixed = kRing + kWarps * kStages * 16 + kWarps * 8 * 8 + kWarps * 32 * 4 + 2 * kQBytes + 16;
+    static constexpr int smem(int B) { return kFixed + (3 * B + 2) * 4; }
 };
 constexpr int kMaxParts = 512;  // CTAs of a launch at most: tickets in the workspace
-constexpr int kMaxDecSeqs = 512;  // sequences of a launch
-static_assert(Dec<128, 1>::smem(kMaxDecSeqs) <= 232448 && Dec<64, 2>::smem(kMaxDecSeqs) <= 232448, "shared memory");
+constexpr int kMaxDecSeqs = 256;  // sequences of a launch
+static_assert(Dec<128, 1>::smem(kMaxDecSeqs) <= 232448 && Dec<64, 1>::smem(kMaxDecSeqs) <= 232448 &&
+                  Dec<128, 2>::smem(kMaxDecSeqs) <= 232448 && Dec<64, 2>::smem(kMaxDecSeqs) <= 232448,
+              "shared memory");
 static_assert(8 * Dec<128, 1>::kPad * 4 <= Dec<128, 1>::kStageBytes, "a warp's O of 8 rows fits a stage");
 
+// The tile of the first place that the first of a sequence's n queries sees.
+template <int TILE>
+__device__ __forceinline__ int first_tile(const AttnArgs& a, int n, int L) {
+    const int lo = a.window > 0 ? L - n + 1 - a.window : 0;
+    return lo > 0 ? lo / TILE : 0;
+}
 // A sequence's queries, context and tiles; bad ones have none.
 struct Seq {
     int64_t row0;
-    int n, L, tile0, per;
+    int n, L, per;
     bool bad;
 };
 template <int TILE>
@@ -73,12 +82,9 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
     s.L = __ldg(a.lens + b);
     s.bad = s.n < 0 || s.n > a.max_q || s.row0 < 0 || s.row0 + s.n > a.total_q || s.L < 0 ||
             (int64_t)s.L > ((int64_t)a.max_pages << a.cache.page_log);
-    s.tile0 = s.per = 0;
+    s.per = 0;
     if (!s.bad && s.n > 0 && s.L > 0) {
-        // the first place that the first query sees
-        const int64_t lo = a.window > 0 ? (int64_t)s.L - s.n + 1 - a.window : 0;
-        s.tile0 = lo > 0 ? (int)(lo / TILE) : 0;
-        s.per = (s.L + TILE - 1) / TILE - s.tile0;
+        s.per = (s.L + TILE - 1) / TILE - first_tile<TILE>(a, s.n, s.L);
     }
     return s;
 }
@@ -135,10 +141,11 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRing);
     uint32_t* bad_groups = reinterpret_cast<uint32_t*>(bars + W * S);
     float2* red = reinterpret_cast<float2*>(bad_groups + 2 * W * S);  // [warp][8 rows] {m, l}
-    uint32_t* source = reinterpret_cast<uint32_t*>(red + W * 8);  // [warp][64] the cache's groups that its next tiles are
-    int* flag = reinterpret_cast<int*>(source + W * 64);
+    uint32_t* source = reinterpret_cast<uint32_t*>(red + W * 8);  // [warp][32] the cache's groups that its next tiles are
+    uint8_t* qbuf = reinterpret_cast<uint8_t*>(source + W * 32);  // [2] this segment's queries and the next one's
+    int* flag = reinterpret_cast<int*>(qbuf + 2 * C::kQBytes);
     int* prefix = flag + 4;  // [B + 1] tiles of one (head, row block) before sequence b
-    int* length = prefix + a.B + 1;
+    int *row0 = prefix + a.B + 1, *length = row0 + a.B + 1;  // [B + 1] first rows of q, [B] contexts
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int HR = a.cache.Hkv * a.RB;
 
@@ -151,7 +158,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
             if (b < a.B) {
                 const Seq s = seq_of<TILE>(a, b);
                 v = s.per;
-                length[b] = s.L;
+                row0[b + 1] = (int)s.row0 + s.n, length[b] = s.L;
                 if (s.bad && blockIdx.x == 0) atomicOr(a.status, kStatusBad);
             }
 #pragma unroll
@@ -162,7 +169,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
             if (b < a.B) prefix[b + 1] = run + v;
             run += __shfl_sync(0xffffffffu, v, 31);
         }
-        if (lane == 0) prefix[0] = 0;
+        if (lane == 0) prefix[0] = 0, row0[0] = __ldg(a.cu);
     }
     fence_mbar_init();
     __syncthreads();
@@ -200,6 +207,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         c.i = (int)(u - (int64_t)c.hr * c.per);
         return c;
     };
+    auto queries = [&](int b) { return row0[b + 1] - row0[b]; };
     auto skip = [&](Cursor& c, int n) {  // n tiles on; the end of the list is not reached
         c.i += n;
         while (c.i >= c.per) {
@@ -223,28 +231,24 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         const int s = issued % S, e = issued % C::kBatch;
         if (e == 0) {
             // where the next kBatch tiles lie, a group a lane: the searches and the page table's latency once for all
-#pragma unroll
-            for (int k = lane; k < 64; k += 32) {
-                uint32_t src = 0xffffffffu;  // behind the end, or a bad page: not copied, and masked
-                if (issued + k / NG < mine) {
-                    const Cursor c = locate(t0 + warp + (int64_t)(issued + k / NG) * W);
-                    const int first = a.window > 0 ? seq_of<TILE>(a, c.b).tile0 : 0;
-                    const int tok = (first + c.i) * TILE + (k % NG) * kGroup;
-                    if (tok < length[c.b]) {
-                        const int page = __ldg(a.table + c.b * a.ldb + (tok >> a.cache.page_log));
-                        if (page >= 0 && page < a.cache.n_pages)
-                            src = (unsigned)page * heads_groups + ((unsigned)(c.hr / a.RB) << (a.cache.page_log - 4)) +
-                                  ((tok & ((1 << a.cache.page_log) - 1)) >> 4);
-                        else
-                            atomicOr(a.status, kStatusBad);
-                    }
+            uint32_t src = 0xffffffffu;  // behind the end, or a bad page: not copied, and masked
+            if (issued + lane / NG < mine) {
+                const Cursor c = locate(t0 + warp + (int64_t)(issued + lane / NG) * W);
+                const int tok = (first_tile<TILE>(a, queries(c.b), length[c.b]) + c.i) * TILE + (lane % NG) * kGroup;
+                if (tok < length[c.b]) {
+                    const int page = __ldg(a.table + c.b * a.ldb + (tok >> a.cache.page_log));
+                    if (page >= 0 && page < a.cache.n_pages)
+                        src = (unsigned)page * heads_groups + ((unsigned)(c.hr / a.RB) << (a.cache.page_log - 4)) +
+                              ((tok & ((1 << a.cache.page_log) - 1)) >> 4);
+                    else
+                        atomicOr(a.status, kStatusBad);
                 }
-                source[warp * 64 + k] = src;
             }
+            source[warp * 32 + lane] = src;
             __syncwarp();
         }
         if (lane < NG) {
-            const uint32_t src = source[warp * 64 + e * NG + lane];
+            const uint32_t src = source[warp * 32 + e * NG + lane];
             uint64_t* bar = &bars[warp * S + s];
             const unsigned ok = __ballot_sync((1u << NG) - 1, src != 0xffffffffu);
             if (lane == 0) bad_groups[warp * S + s] = ~ok & ((1u << NG) - 1);
@@ -256,69 +260,74 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         __syncwarp();
         ++issued;
     };
-    // one stage stays free: the last one read, which holds the warp's O while the warps' parts are joined
-    for (int k = 0; k < S - 1 && k < mine; ++k) issue();
-
-    Cursor seg = locate(t0), cc = locate(mine > 0 ? t0 + warp : t0);
+    Cursor seg = locate(t0), cc = seg;
+    if (mine > 0) skip(cc, warp);
     int64_t s0 = t0 - seg.i;  // the first tile of this (sequence, head, row block)
     int done = 0;
     bool failed = false;
-    for (;;) {
-        const Seq q = seq_of<TILE>(a, seg.b);
+    // The queries of a segment go to shared memory as fp16, scaled by a power of two (with the sign of the scale) that
+    // puts the row's largest magnitude in [2^14, 2^15): exact but for values 2^28 below it.  A row's D / 8 lanes hold 8
+    // values each; lane (g, t) of a product later reads its values (D / 4) t + 8 w .. + 7 of row g as one 16 bytes.
+    constexpr int LPR = D / 8;
+    const int qr = threadIdx.x / LPR, qd = threadIdx.x % LPR * 8;
+    auto load_q = [&](const Cursor& c) {
+        const int rr = c.hr % a.RB * C::kRows + qr;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (qr < C::kRows && rr < queries(c.b) * a.G)
+            u = __ldg(reinterpret_cast<const uint4*>(a.q + ((int64_t)row0[c.b] + rr / a.G) * a.ldq +
+                                                     (int64_t)(c.hr / a.RB * a.G + rr % a.G) * D + qd));
+        return u;
+    };
+    auto store_q = [&](const uint4& u, uint8_t* to) {
+        if (threadIdx.x >= (C::kRows * LPR + 31) / 32 * 32) return;
+        const uint32_t raw[4] = {u.x, u.y, u.z, u.w};
+        float mx = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(raw[k] << 16)), fabsf(__uint_as_float(raw[k] & 0xffff0000u))));
+#pragma unroll
+        for (int k = LPR / 2; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+        // exponent of the largest magnitude, kept where both 2^(14 - e) and 2^(e - 14) are normal numbers
+        const int e = max(min((int)(__float_as_uint(mx) >> 23) - 127, 126), -100);
+        const float up = copysignf(__uint_as_float((uint32_t)(14 - e + 127) << 23), a.scale_log2);
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            h[k] = pack_f16x2(__uint_as_float(raw[k] << 16) * up, __uint_as_float(raw[k] & 0xffff0000u) * up);
+        const int at = ((qd % (D / 4) / 8 * C::kRows + qr) * 4 + qd / (D / 4)) * 16;
+        *reinterpret_cast<uint4*>(to + at) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (qd == 0)
+            reinterpret_cast<float*>(to + C::kRows * D * 2)[qr] =
+                fabsf(a.scale_log2) * __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+    };
+    uint4 qnext = load_q(seg);  // in flight with the first copies
+    // one stage stays free: the last one read, which holds the warp's O while the warps' parts are joined
+    for (int k = 0; k < S - 1 && k < mine; ++k) issue();
+    store_q(qnext, qbuf);
+    __syncthreads();
+
+    for (int turn = 0;; turn ^= 1) {
+        const int qn = queries(seg.b), qL = length[seg.b], tile0 = first_tile<TILE>(a, qn, qL);
+        const int64_t qrow = row0[seg.b];
         const int h = seg.hr / a.RB, rb = seg.hr % a.RB;
-        const int rows = min(C::kRows, q.n * a.G - rb * C::kRows);  // may be <= 0
+        const int rows = min(C::kRows, qn * a.G - rb * C::kRows);  // may be <= 0
         const int64_t s1 = s0 + seg.per;
-        // the queries as the columns' operand: column g of lane (g, t) holds values (D / 4) t .. of row g, as fp16
-        // scaled by a power of two (with the sign of the scale) that puts the row's largest magnitude in
-        // [2^14, 2^15): exact but for values 2^28 below it.  rs takes the scores to the exponents of 2.
-        uint32_t qf[NT][KS][2];
-        float rs[NT][2], m[NT][2], l[NT][2];
+        const uint8_t* qs = qbuf + turn * C::kQBytes;
+        float rs[NT][2], m[NT][2], l[NT][2];  // rs takes the scores to the exponents of 2
         int hi[NT][2];
         float o[KS][NT][4];
         const bool any = done < mine && cc.b == seg.b && cc.hr == seg.hr;
         if (any) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int r = nt * 8 + g, rr = rb * C::kRows + r;
-                uint32_t raw[KS * 2];
-                float mx = 0.f;
-                if (r < rows) {
-                    const __nv_bfloat16* p =
-                        a.q + (q.row0 + rr / a.G) * a.ldq + (int64_t)(h * a.G + rr % a.G) * D + t * (D / 4);
-#pragma unroll
-                    for (int k = 0; k < KS / 2; ++k) {
-                        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + k);
-                        raw[4 * k] = u.x, raw[4 * k + 1] = u.y, raw[4 * k + 2] = u.z, raw[4 * k + 3] = u.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < KS * 2; ++k) raw[k] = 0u;
-                }
-#pragma unroll
-                for (int k = 0; k < KS * 2; ++k)
-                    mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(raw[k] << 16)), fabsf(__uint_as_float(raw[k] & 0xffff0000u))));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                // exponent of the largest magnitude, kept where both 2^(14 - e) and 2^(e - 14) are normal numbers
-                const int e = max(min((int)(__float_as_uint(mx) >> 23) - 127, 126), -100);
-                const float up = copysignf(__uint_as_float((uint32_t)(14 - e + 127) << 23), a.scale_log2);
-                const float down = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(e - 14 + 127) << 23);
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const uint32_t w = raw[2 * k + c];
-                        qf[nt][k][c] = pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
-                    }
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    rs[nt][c] = __shfl_sync(0xffffffffu, down, (2 * t + c) * 4);
-                    const int row = rb * C::kRows + nt * 8 + 2 * t + c;
-                    hi[nt][c] = q.L - q.n + row / a.G;  // the last place that the column's query sees
+                    const int r = nt * 8 + 2 * t + c;
+                    rs[nt][c] = reinterpret_cast<const float*>(qs + C::kRows * D * 2)[r];
+                    hi[nt][c] = qL - qn + (rb * C::kRows + r) / a.G;  // the last place that the column's query sees
                     m[nt][c] = -INFINITY;
                     l[nt][c] = 0.f;
                 }
-            }
 #pragma unroll
             for (int i = 0; i < KS; ++i)
 #pragma unroll
@@ -334,7 +343,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                 mine = issued;  // nothing more is copied; what is in flight is waited for
             }
             const uint8_t* st = ring + s * C::kStageBytes;
-            const int tok0 = (q.tile0 + cc.i) * TILE;
+            const int tok0 = (tile0 + cc.i) * TILE;
             const uint32_t bad = bad_groups[warp * S + s];
             // every row sees all of the tile's tokens, unless the tile reaches past the first row's place or
             // before the last one's window: the common form has no masks at all
@@ -342,44 +351,51 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                 constexpr bool edge = decltype(masked)::value;
                 // S^T: rows g and g + 8 of a group's 16 are its tokens ta and ta + 2
                 const int ta = 4 * (g >> 1) + (g & 1);
+                constexpr int WK = D / 32;  // words of codes a lane has of a token
                 float sc[NG][NT][4];
+                uint32_t w0[NG][WK], w1[NG][WK], f0[NG][D / 64], f1[NG][D / 64];
 #pragma unroll
                 for (int gr = 0; gr < NG; ++gr) {
                     const uint8_t* gp = st + gr * group_bytes(D);
-                    uint32_t w0[D / 32], w1[D / 32], f0[D / 64], f1[D / 64];
                     if constexpr (D == 128) {
                         const uint4 x = lds128(gp + ta * 64 + t * 16), y = lds128(gp + (ta + 2) * 64 + t * 16);
-                        w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
-                        w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
+                        w0[gr][0] = x.x, w0[gr][1] = x.y, w0[gr][2] = x.z, w0[gr][3] = x.w;
+                        w1[gr][0] = y.x, w1[gr][1] = y.y, w1[gr][2] = y.z, w1[gr][3] = y.w;
                         const uint32_t z0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(gp + k_scale_off(D) + ta * 8 + t * 2));
                         const uint32_t z1 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(gp + k_scale_off(D) + (ta + 2) * 8 + t * 2));
-                        f0[0] = __byte_perm(z0, 0, 0x1010), f0[1] = __byte_perm(z0, 0, 0x3232);
-                        f1[0] = __byte_perm(z1, 0, 0x1010), f1[1] = __byte_perm(z1, 0, 0x3232);
+                        f0[gr][0] = __byte_perm(z0, 0, 0x1010), f0[gr][1] = __byte_perm(z0, 0, 0x3232);
+                        f1[gr][0] = __byte_perm(z1, 0, 0x1010), f1[gr][1] = __byte_perm(z1, 0, 0x3232);
                     } else {
                         const uint2 x = *reinterpret_cast<const uint2*>(gp + ta * 32 + t * 8);
                         const uint2 y = *reinterpret_cast<const uint2*>(gp + (ta + 2) * 32 + t * 8);
-                        w0[0] = x.x, w0[1] = x.y;
-                        w1[0] = y.x, w1[1] = y.y;
+                        w0[gr][0] = x.x, w0[gr][1] = x.y;
+                        w1[gr][0] = y.x, w1[gr][1] = y.y;
                         const uint32_t z = e4m3x2_to_f16x2((uint32_t)gp[k_scale_off(D) + ta * 4 + t] |
                                                            (uint32_t)gp[k_scale_off(D) + (ta + 2) * 4 + t] << 8);
-                        f0[0] = __byte_perm(z, 0, 0x1010), f1[0] = __byte_perm(z, 0, 0x3232);
+                        f0[gr][0] = __byte_perm(z, 0, 0x1010), f1[gr][0] = __byte_perm(z, 0, 0x3232);
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) sc[gr][nt][c] = 0.f;
+                }
 #pragma unroll
-                    for (int w = 0; w < D / 32; ++w) {  // a word of codes: two steps of the inner axis
+                for (int w = 0; w < WK; ++w) {  // a word of codes: two steps of the inner axis
+                    uint4 qf[NT];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) qf[nt] = lds128(qs + ((w * C::kRows + nt * 8 + g) * 4 + t) * 16);
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr) {
                         uint32_t h0[4], h1[4];
-                        e2m1x8(w0[w], h0);
-                        e2m1x8(w1[w], h1);
+                        e2m1x8(w0[gr][w], h0);
+                        e2m1x8(w1[gr][w], h1);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) h0[c] = hmul2(h0[c], f0[w / 2]), h1[c] = hmul2(h1[c], f1[w / 2]);
+                        for (int c = 0; c < 4; ++c) h0[c] = hmul2(h0[c], f0[gr][w / 2]), h1[c] = hmul2(h1[c], f1[gr][w / 2]);
+                        const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const uint32_t af[4] = {h0[2 * u], h1[2 * u], h0[2 * u + 1], h1[2 * u + 1]};
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma16816(sc[gr][nt], af, qf[nt][2 * w + u][0], qf[nt][2 * w + u][1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816(sc[gr][nt], a0, qf[nt].x, qf[nt].y);
+                            mma16816(sc[gr][nt], a1, qf[nt].z, qf[nt].w);
                         }
                     }
                 }
@@ -391,7 +407,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
                                 const int tok = tok0 + gr * kGroup + ta + (c & 2);
-                                const bool sees = tok <= hi[nt][c & 1] && tok < q.L && !((bad >> gr) & 1) &&
+                                const bool sees = tok <= hi[nt][c & 1] && tok < qL && !((bad >> gr) & 1) &&
                                                   (a.window == 0 || tok > hi[nt][c & 1] - a.window);
                                 sc[gr][nt][c] = sees ? sc[gr][nt][c] : -INFINITY;
                             }
@@ -476,7 +492,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                     }
                     uint32_t vs = *reinterpret_cast<const uint32_t*>(gp + v_scale_off(D) + blk * 16 + t * 4);
                     if constexpr (edge) {  // places behind the end hold anything: scale 0, so that 0 * value is 0
-                        const int left = (bad >> gr) & 1 ? 0 : q.L - (tok0 + gr * kGroup + 4 * t);
+                        const int left = (bad >> gr) & 1 ? 0 : qL - (tok0 + gr * kGroup + 4 * t);
                         vs = left >= 4 ? vs : left <= 0 ? 0u : vs & ((1u << (8 * left)) - 1u);
                     }
                     const uint32_t f01 = e4m3x2_to_f16x2(vs & 0xffffu), f23 = e4m3x2_to_f16x2(vs >> 16);
@@ -497,7 +513,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                     }
                 }
             };
-            if (bad != 0 || tok0 + TILE - 1 > q.L - q.n || (a.window > 0 && tok0 <= q.L - 1 - a.window))
+            if (bad != 0 || tok0 + TILE - 1 > qL - qn || (a.window > 0 && tok0 <= qL - 1 - a.window))
                 step(cuda::std::true_type());
             else
                 step(cuda::std::false_type());
@@ -507,6 +523,13 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
             if (issued < mine) issue();  // into the stage that was read before this one
         }
 
+        // the next segment's queries: in flight while this one's parts are joined
+        const bool last = s1 >= t1;
+        if (!last) {
+            seg.i = 0;
+            skip(seg, seg.per);
+            qnext = load_q(seg);
+        }
         // join the warps' parts, 8 rows at a time, in the order of the warps
         const int c0 = (int)(((s0 + 1) * P - 1) / T), c1 = (int)((s1 * P - 1) / T);
         const bool whole = c0 == c1;
@@ -557,7 +580,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                 if (whole) {
                     const float inv = sum > 0.f ? a.cache.v_scale / sum : 0.f;
                     const int rr = rb * C::kRows + nt * 8 + r;
-                    *reinterpret_cast<__nv_bfloat162*>(a.out + (q.row0 + rr / a.G) * a.ldo +
+                    *reinterpret_cast<__nv_bfloat162*>(a.out + (qrow + rr / a.G) * a.ldo +
                                                        (int64_t)(h * a.G + rr % a.G) * D + 2 * pair) =
                         __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
                 } else {
@@ -579,42 +602,93 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
             }
             __syncthreads();
             if (*flag) {
+                // a row a warp; where the rows are fewer than the warps, each takes every nsp-th part of its row
+                constexpr int V = D / 32;  // values a lane
                 const int64_t psz = (int64_t)C::kRows * (D + 2);
-                for (int e = threadIdx.x; e < rows * D / 2; e += W * 32) {
-                    const int r = e / (D / 2), pair = e % (D / 2);
-                    float M = -INFINITY, sum = 0.f;
-                    for (int c = c0; c <= c1; ++c)
-                        M = fmaxf(M, __ldcg(a.parts + (2 * c + (c == c0)) * psz + C::kRows * D + 2 * r));
-                    float2 acc = make_float2(0.f, 0.f);
-                    if (M != -INFINITY) {
-#pragma unroll 4
-                        for (int c = c0; c <= c1; ++c) {
-                            const float* p = a.parts + (2 * c + (c == c0)) * psz;
-                            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + C::kRows * D + 2 * r));
-                            const float2 v = __ldcg(reinterpret_cast<const float2*>(p + r * D + 2 * pair));
-                            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-                            acc.x += f * v.x, acc.y += f * v.y;
-                            sum += f * ml.y;
+                int rp = 1;
+                while (rp < rows && rp < W) rp *= 2;
+                const int nsp = W / rp, sp = warp / rp;
+                float* mo = reinterpret_cast<float*>(ring + ((done + S - 1) % S) * C::kStageBytes);
+                for (int r = warp % rp; r < C::kRows; r += rp) {
+                    float M = -INFINITY, sum = 0.f, acc[V];
+#pragma unroll
+                    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+                    if (r < rows) {
+                        constexpr int U = 4;  // parts in flight
+                        for (int c = c0 + sp; c <= c1; c += U * nsp) {
+                            float2 ml[U], v[U][V / 2];
+#pragma unroll
+                            for (int u = 0; u < U; ++u) {
+                                const int cu = c + u * nsp;
+                                ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                                for (int k = 0; k < V / 2; ++k) v[u][k] = make_float2(0.f, 0.f);
+                                if (cu > c1) continue;
+                                const float* p = a.parts + (2 * cu + (cu == c0)) * psz;
+                                ml[u] = __ldcg(reinterpret_cast<const float2*>(p + C::kRows * D + 2 * r));
+#pragma unroll
+                                for (int k = 0; k < V / 2; ++k)
+                                    v[u][k] = __ldcg(reinterpret_cast<const float2*>(p + r * D + lane * V + 2 * k));
+                            }
+                            float mn = M;
+#pragma unroll
+                            for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[u].x);
+                            const float top = mn == -INFINITY ? 0.f : mn, f0 = ex2(M - top);
+                            M = mn;
+                            sum *= f0;
+#pragma unroll
+                            for (int k = 0; k < V; ++k) acc[k] *= f0;
+#pragma unroll
+                            for (int u = 0; u < U; ++u) {
+                                const float f = ex2(ml[u].x - top);
+                                sum += f * ml[u].y;
+#pragma unroll
+                                for (int k = 0; k < V / 2; ++k)
+                                    acc[2 * k] += f * v[u][k].x, acc[2 * k + 1] += f * v[u][k].y;
+                            }
                         }
                     }
-                    const float inv = sum > 0.f ? a.cache.v_scale / sum : 0.f;
-                    const int rr = rb * C::kRows + r;
-                    *reinterpret_cast<__nv_bfloat162*>(a.out + (q.row0 + rr / a.G) * a.ldo +
-                                                       (int64_t)(h * a.G + rr % a.G) * D + 2 * pair) =
-                        __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+                    if (nsp > 1) {
+                        if (lane == 0) red[warp] = make_float2(M, sum);
+#pragma unroll
+                        for (int k = 0; k < V; ++k) mo[lane * V + k] = acc[k];
+                        __syncthreads();
+                        if (sp == 0 && r < rows) {
+                            float mn = M;
+                            for (int w = warp + rp; w < W; w += rp) mn = fmaxf(mn, red[w].x);
+                            const float top = mn == -INFINITY ? 0.f : mn, f0 = ex2(M - top);
+                            sum *= f0;
+#pragma unroll
+                            for (int k = 0; k < V; ++k) acc[k] *= f0;
+                            for (int w = warp + rp; w < W; w += rp) {
+                                const float f = ex2(red[w].x - top);
+                                const float* p = reinterpret_cast<const float*>(smem + (w * S + bad_groups[W * S + w]) * C::kStageBytes);
+                                sum += f * red[w].y;
+#pragma unroll
+                                for (int k = 0; k < V; ++k) acc[k] += f * p[lane * V + k];
+                            }
+                        }
+                        __syncthreads();
+                    }
+                    if (sp == 0 && r < rows) {
+                        const float inv = sum > 0.f ? a.cache.v_scale / sum : 0.f;
+                        const int rr = rb * C::kRows + r;
+                        __nv_bfloat16* dst = a.out + (qrow + rr / a.G) * a.ldo + (int64_t)(h * a.G + rr % a.G) * D + lane * V;
+#pragma unroll
+                        for (int k = 0; k < V; k += 2)
+                            *reinterpret_cast<__nv_bfloat162*>(dst + k) = __floats2bfloat162_rn(acc[k] * inv, acc[k + 1] * inv);
+                    }
                 }
             }
         }
+        if (last) break;
+        store_q(qnext, qbuf + (turn ^ 1) * C::kQBytes);
         // the joining wrote stages that bulk copies fill next
         fence_proxy_async_smem();
         __syncthreads();
-        if (s1 >= t1) break;
-        seg.i = 0;
-        skip(seg, seg.per);
         s0 = s1;
     }
 }
-
 
 template <int D>
 __global__ void __launch_bounds__(128) attn_simple_kernel(const AttnArgs a) {
