@@ -1,0 +1,702 @@
+// attn_chunk.cu -- attention of prompt chunks over the paged NVFP4 cache on the 5th-generation tensor cores.
+//
+// A unit is 256 query rows of one (sequence, kv head): row r is query r / G, head r % G of the group, so that every
+// group size fills the tiles and K and V are dequantized once for all heads that share them.  A CTA (one an SM) works
+// on a unit's two tiles of 128 rows against 128 tokens at a time, tcgen05.mma kind::f16 with fp32 accumulators in tensor
+// memory:
+//   warps 0-3, 4-7: softmax of tile A and of tile B, a row a thread: scores from tensor memory, exponentials,
+//                   probabilities back as the fp16 A operand of P V (in the scores' columns); they also bring the
+//                   queries in (fp16, row_exponent) and take O out;
+//   warps 8-11    : dequantize K ([token][value], a token a thread) and V (transposed, [value][token], 16 values x 8
+//                   tokens a thread) into 128-byte-swizzled K-major tiles, two stages each, the next tile's codes
+//                   already in registers;
+//   warp 12       : one thread issues the products, S_A, S_B, then per tile of tokens P V of A, the next S_A, P V of B, the
+//                   next S_B: the tensor cores work for one tile while the other's softmax runs.
+// The exponent's reference follows the running maximum only when that has grown by 2^8, so O is rarely rescaled.
+// Units are dealt out heaviest first, there and back; those of the last, partial round are split along the tokens
+// where that shortens it, and the last CTA of a unit to finish joins its parts in their order.
+// Every wait is bounded; a timeout sets the status word and the CTA winds down.
+#include <cuda/std/type_traits>
+
+#include "attn_common.cuh"
+
+namespace qlin {
+namespace kv {
+
+namespace ch {
+
+constexpr int kRows = 256, kTok = 128;
+constexpr int kSoftWarps = 8, kDqWarps = 4;
+constexpr int kThreads = (kSoftWarps + kDqWarps + 1) * 32;
+constexpr int kMaxSeqs = 1024;
+constexpr int kSplitCost = 3;  // tiles that a split's queries, rows and joining cost
+
+template <int D>
+struct Cfg {
+    static constexpr int kQBytes = 128 * D * 2;  // one tile of queries
+    static constexpr int kKBytes = kTok * D * 2, kVBytes = kTok * D * 2;
+    static constexpr int kSmem = 1024 + 2 * kQBytes + 2 * kKBytes + 2 * kVBytes + 512;
+    static constexpr int smem(int B) { return kSmem + (3 * B + 2) * 4; }
+};
+static_assert(Cfg<128>::smem(kMaxSeqs) <= 232448, "shared memory");
+
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr) {  // K-major, 128-byte swizzle
+    uint64_t d = (uint64_t)((saddr >> 4) & 0x3fffu);
+    d |= (uint64_t)1 << 16;            // leading byte offset (unused for swizzled K-major)
+    d |= (uint64_t)(1024 >> 4) << 32;  // stride byte offset: 8-row groups 1024 B apart
+    d |= (uint64_t)1 << 46;            // descriptor version for sm_100
+    d |= (uint64_t)2 << 61;            // 128-byte swizzle
+    return d;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void ld32(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+        "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// A piece of work: 256 rows of one (sequence, kv head) from row `base`, tiles [t0, t1) of 128 tokens.
+struct Item {
+    int b, h, base, rows, n, L, t0, t1;
+    int64_t row0;
+    int part, parts;  // part of a unit that several CTAs share (parts > 1)
+    int tail;         // its number among the shared ones
+};
+
+}  // namespace ch
+
+template <int D>
+__global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnArgs a) {
+    using namespace ch;
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t* qt = smem;
+    uint8_t* kt = qt + 2 * C::kQBytes;
+    uint8_t* vt = kt + 2 * C::kKBytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(vt + 2 * C::kVBytes);
+    uint64_t *qfull = bars, *kfull = bars + 2, *kfree = bars + 4, *vfull = bars + 6, *vfree = bars + 8, *sfull = bars + 10,
+             *pfull = bars + 12, *ofull = bars + 14, *mma_done = bars + 16;
+    uint8_t* bad = reinterpret_cast<uint8_t*>(bars + 17);  // [4][8]: groups of a tile that a bad page leaves out
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 21);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    int* last_flag = reinterpret_cast<int*>(tmem_holder + 2);
+    int* tail_tiles = reinterpret_cast<int*>(tmem_holder + 3);  // of all units of the last round
+    int* prefix = reinterpret_cast<int*>(bars + 64);      // [B + 1] units of one kv head before sequence b
+    int *row0 = prefix + a.B + 1, *length = row0 + a.B + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int Hkv = a.cache.Hkv;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&qfull[i], 128);
+            mbar_init(&kfull[i], kDqWarps * 32);
+            mbar_init(&vfull[i], kDqWarps * 32);
+            mbar_init(&kfree[i], 1);
+            mbar_init(&vfree[i], 1);
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pfull[i], 128);
+            mbar_init(&ofull[i], 1);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        *tail_tiles = 0;
+        fence_mbar_init();
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_holder)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (warp == 0) {
+        int run = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            const int b = b0 + lane;
+            int v = 0;
+            if (b < a.B) {
+                const Seq s = seq_of(a, b);
+                if (!s.bad) v = (int)(((int64_t)s.n * a.G + kRows - 1) / kRows);
+                row0[b + 1] = (int)s.row0 + s.n, length[b] = s.L;
+                if (s.bad && blockIdx.x == 0) atomicOr(a.status, kStatusBad);
+            }
+#pragma unroll
+            for (int k = 1; k < 32; k <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, k);
+                if (lane >= k) v += u;
+            }
+            if (b < a.B) prefix[b + 1] = run + v;
+            run += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) prefix[0] = 0, row0[0] = __ldg(a.cu);
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tmem_holder;
+
+    // unit u: sequences in order; in each the last rows first (the most tokens), the kv heads of a block side by side
+    auto unit = [&](int u) {
+        Item it;
+        int lo = 0, hi = a.B - 1;  // the last b with prefix[b] * Hkv <= u (it has units)
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((int64_t)prefix[mid] * Hkv <= u) lo = mid;
+            else hi = mid - 1;
+        }
+        const int k = u - prefix[lo] * Hkv, blocks = prefix[lo + 1] - prefix[lo];
+        it.b = lo;
+        it.h = k % Hkv;
+        it.base = (blocks - 1 - k / Hkv) * kRows;
+        it.n = row0[lo + 1] - row0[lo];
+        it.L = length[lo];
+        it.row0 = row0[lo];
+        it.rows = min(kRows, it.n * a.G - it.base);
+        const int p0 = it.L - it.n + it.base / a.G, p1 = it.L - it.n + (it.base + it.rows - 1) / a.G;
+        const int first = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
+        it.t0 = first / kTok;
+        it.t1 = p1 < 0 ? it.t0 : p1 / kTok + 1;
+        it.part = 0, it.parts = 1, it.tail = -1;
+        return it;
+    };
+    const int64_t units64 = (int64_t)prefix[a.B] * Hkv;
+    const int units = (int)units64;
+    const int grid = gridDim.x, whole = units / grid * grid, tails = units - whole;
+    // splits of the last round's units: their rounds times a part's tiles and its fixed cost, the least of it
+    for (int i = threadIdx.x; i < tails; i += kThreads) {
+        const Item it = unit(whole + i);
+        atomicAdd(tail_tiles, it.t1 - it.t0);
+    }
+    __syncthreads();
+    int splits = 1;
+    if (tails > 0) {
+        const float avg = (float)*tail_tiles / tails;
+        float best = avg + kSplitCost;
+        for (int s = 2; s <= 32 && tails * s <= 2 * grid; ++s) {
+            const float cost = (float)((tails * s + grid - 1) / grid) * (avg / s + kSplitCost) + kSplitCost;
+            if (cost < best && avg >= 2 * s) best = cost, splits = s;
+        }
+    }
+    const int items = whole + tails * splits;
+    auto item = [&](int k) {  // the k-th of this CTA: rounds go there and back
+        const int i = k * grid + ((k & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        if (i >= items) {
+            Item none = {};
+            none.b = -1;
+            return none;
+        }
+        if (i < whole || splits == 1) return unit(i);
+        const int r = (i - whole) / splits, s = (i - whole) % splits;
+        Item it = unit(whole + r);
+        const int cnt = it.t1 - it.t0, first = it.t0;
+        it.t0 = first + (int)((int64_t)cnt * s / splits);
+        it.t1 = first + (int)((int64_t)cnt * (s + 1) / splits);
+        it.part = s, it.parts = splits, it.tail = r;
+        return it;
+    };
+    const int rounds = (items + grid - 1) / grid;
+    auto wait = [&](uint64_t* bar, int parity) {  // false: gave up, or another warp has
+        if (*abort_flag) return false;
+        if (mbar_wait_bounded(bar, parity)) return true;
+        atomicOr(a.status, 1u);
+        *abort_flag = 1;
+        return false;
+    };
+
+    if (warp < kSoftWarps) {
+        const int x = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane, srow = x * 128 + row;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + 256 + x * D;
+        uint8_t* qx = qt + x * C::kQBytes;
+        int tiles = 0, its = 0;  // of this tile of rows so far: the barriers' phases
+        bool ok = true;          // after a wait that gave up: no more products, but every barrier of the eight warps
+        auto warp_wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+        int all_tiles = 0;       // of the CTA: the bad groups' ring
+        for (int k = 0; k < rounds; ++k) {
+            const Item it = item(k);
+            if (it.b < 0) continue;
+            const int cnt = it.t1 - it.t0;
+            const int r = it.base + srow, tok = r / a.G;
+            const bool valid = srow < it.rows;
+            const int64_t qrow = it.row0 + tok;
+            const int head = it.h * a.G + r % a.G;
+            const int p = it.L - it.n + tok;  // the last place this row sees
+            // of this warp's rows: the first one's and the last one's
+            const int pw0 = it.L - it.n + (it.base + x * 128 + quarter * 32) / a.G;
+            const int pw1 = it.L - it.n + (it.base + x * 128 + quarter * 32 + 31) / a.G;
+            float rs = 0.f, m = -INFINITY, l = 0.f;
+            const bool active = x * 128 < it.rows && cnt > 0 && ok;
+            if (active) {
+                // queries: the row as fp16, 16-byte pieces of 128-byte rows turned by the row
+                uint32_t w[D / 2];
+                float mx = 0.f;
+                if (valid) {
+                    const uint4* src = reinterpret_cast<const uint4*>(a.q + qrow * a.ldq + (int64_t)head * D);
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 u = __ldg(src + i);
+                        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 2; ++i) w[i] = 0u;
+                }
+#pragma unroll
+                for (int i = 0; i < D / 2; ++i) mx = fmaxf(mx, amax_bf16x2(w[i]));
+                const int e = row_exponent(mx);
+                const float up = row_up(e, a.scale_log2);
+                rs = row_down(e, a.scale_log2);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    *reinterpret_cast<uint4*>(qx + (i >> 3) * (128 * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
+                        make_uint4(scaled_f16x2(w[4 * i], up), scaled_f16x2(w[4 * i + 1], up),
+                                   scaled_f16x2(w[4 * i + 2], up), scaled_f16x2(w[4 * i + 3], up));
+                fence_proxy_async_smem();
+                arrive(&qfull[x]);
+                for (int j = 0; j < cnt; ++j) {
+                    ok = warp_wait(&sfull[x], tiles & 1);
+                    if (!ok) break;
+                    ++tiles;
+                    fence_after();
+                    const int tok0 = (it.t0 + j) * kTok;
+                    const uint64_t out = *reinterpret_cast<const volatile uint64_t*>(bad + ((all_tiles + j) & 3) * 8);
+                    const bool edge = out != 0 || tok0 + kTok - 1 > pw0 || (a.window > 0 && tok0 <= pw1 - a.window);
+                    uint32_t pk[64];
+                    // one pass with the reference as it is; a second one where a score is more than 2^8 above it
+                    auto pass = [&](auto masked, auto only_max, float ref) {
+                        float top = -INFINITY;
+                        float2 sum = make_float2(0.f, 0.f);
+                        const float2 rs2 = make_float2(rs, rs), ref2 = make_float2(-ref, -ref);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            float v[32];
+                            ld32(ts + 32 * c, v);
+                            if constexpr (decltype(masked)::value) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) {
+                                    const int tk = tok0 + 32 * c + i;
+                                    const bool sees = tk <= p && (a.window == 0 || tk > p - a.window) &&
+                                                      !((out >> (8 * ((32 * c + i) >> 4))) & 1);
+                                    v[i] = sees ? v[i] : -INFINITY;
+                                }
+                            }
+                            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                t0 = fmaxf(t0, fmaxf(v[i], v[i + 1]));
+                                t1 = fmaxf(t1, fmaxf(v[i + 2], v[i + 3]));
+                            }
+                            top = fmaxf(top, fmaxf(t0, t1));
+                            if constexpr (!decltype(only_max)::value) {
+#pragma unroll
+                                for (int i = 0; i < 32; i += 2) {
+                                    // The careful form rounds twice, as the reference does: the largest score's exponent
+                                    // is 0 whatever its size.  One rounding leaves up to half an ulp of the reference there,
+                                    // less than 1 below 2^24, the same for the whole row.
+                                    float2 y;
+                                    if constexpr (decltype(masked)::value)
+                                        y = make_float2(__fsub_rn(__fmul_rn(v[i], rs), ref), __fsub_rn(__fmul_rn(v[i + 1], rs), ref));
+                                    else
+                                        y = __ffma2_rn(make_float2(v[i], v[i + 1]), rs2, ref2);
+                                    float2 e2 = make_float2(ex2(y.x), ex2(y.y));
+                                    if constexpr (decltype(masked)::value) {  // also where rs is 0
+                                        e2.x = v[i] == -INFINITY ? 0.f : e2.x;
+                                        e2.y = v[i + 1] == -INFINITY ? 0.f : e2.y;
+                                    }
+                                    sum = __fadd2_rn(sum, e2);
+                                    pk[16 * c + i / 2] = pack_f16x2(e2.x, e2.y);
+                                }
+                            }
+                        }
+                        return make_float2(top == -INFINITY ? top : __fmul_rn(top, rs), sum.x + sum.y);
+                    };
+                    const cuda::std::true_type yes;
+                    const cuda::std::false_type no;
+                    float2 got;
+                    bool again = __any_sync(0xffffffffu, m == -INFINITY);
+                    for (;;) {
+                        if (again) {
+                            const float top = edge ? pass(yes, yes, 0.f).x : pass(no, yes, 0.f).x;
+                            const float mn = fmaxf(m, top);
+                            const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+                            m = mn;
+                            l *= f;
+                            if (j > 0) {  // the products before this tile are done: S of this tile came after them
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 32) {
+                                    float v[32];
+                                    ld32(to + c, v);
+                                    uint32_t u[32];
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * f);
+                                    st32(to + c, u);
+                                }
+                            }
+                        }
+                        const float ref = m == -INFINITY ? 0.f : m;
+                        const bool careful = edge || __any_sync(0xffffffffu, fabsf(ref) >= 0x1p24f);
+                        got = careful ? pass(yes, no, ref) : pass(no, no, ref);
+                        if (again || !__any_sync(0xffffffffu, got.x > m + 8.f)) break;
+                        again = true;
+                    }
+                    l += got.y;
+                    st32(ts, pk);
+                    st32(ts + 32, pk + 32);
+                    st_wait();
+                    fence_before();
+                    arrive(&pfull[x]);
+                }
+                ok = ok && warp_wait(&ofull[x], its & 1);
+                ++its;
+                fence_after();
+            }
+            all_tiles += cnt;
+            // O: to its rows, or as this part's sums
+            const int64_t slot = it.parts > 1 ? (int64_t)(it.tail * it.parts + it.part) : 0;
+            float* part = a.parts + slot * kRows * (D + 2);  // [D / 4][256 rows] of four values, then [256] {m, l}
+            const float inv = l > 0.f ? a.cache.v_scale / l : 0.f;
+            __nv_bfloat16* dst = a.out + qrow * a.ldo + (int64_t)head * D;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                float v[32];
+                if (active && ok) {
+                    ld32(to + c, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                }
+                if (!valid) continue;
+                if (it.parts == 1) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t u[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[i + 2 * q] * inv, v[i + 2 * q + 1] * inv);
+                            u[q] = *reinterpret_cast<const uint32_t*>(&b2);
+                        }
+                        *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        __stcg(reinterpret_cast<float4*>(part) + (c + i) / 4 * kRows + srow,
+                               make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+                }
+            }
+            fence_before();  // O is read before the next unit's products (the queries' barrier)
+            if (it.parts > 1) {
+                if (valid) __stcg(reinterpret_cast<float2*>(part + (int64_t)kRows * D) + srow, make_float2(m, l));
+                __threadfence();
+                soft_sync();
+                if (threadIdx.x == 0) {
+                    const int before = atomicAdd(&a.tickets[it.tail], 1);
+                    *last_flag = before == it.parts - 1;
+                    if (*last_flag) a.tickets[it.tail] = 0;  // everyone has come: zero for the next call
+                    __threadfence();
+                }
+                soft_sync();
+                if (*last_flag && valid) {
+                    const float* base = a.parts + (int64_t)it.tail * it.parts * kRows * (D + 2);
+                    float mj = -INFINITY, lj = 0.f;
+                    for (int s = 0; s < it.parts; ++s)
+                        mj = fmaxf(mj, __ldcg(reinterpret_cast<const float2*>(base + (int64_t)s * kRows * (D + 2) + (int64_t)kRows * D) + srow).x);
+                    const float ref = mj == -INFINITY ? 0.f : mj;
+                    for (int s = 0; s < it.parts; ++s) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(base + (int64_t)s * kRows * (D + 2) + (int64_t)kRows * D) + srow);
+                        lj += ml.y * ex2(ml.x - ref);
+                    }
+                    const float invj = lj > 0.f ? a.cache.v_scale / lj : 0.f;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        float4 acc[4] = {};
+                        for (int s = 0; s < it.parts; ++s) {
+                            const float* ps = base + (int64_t)s * kRows * (D + 2);
+                            const float f = ex2(__ldcg(reinterpret_cast<const float2*>(ps + (int64_t)kRows * D) + srow).x - ref);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float4 v = __ldcg(reinterpret_cast<const float4*>(ps) + (c / 4 + i) * kRows + srow);
+                                acc[i].x += f * v.x, acc[i].y += f * v.y, acc[i].z += f * v.z, acc[i].w += f * v.w;
+                            }
+                        }
+                        uint32_t u[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[i].x * invj, acc[i].y * invj);
+                            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[i].z * invj, acc[i].w * invj);
+                            u[2 * i] = *reinterpret_cast<const uint32_t*>(&lo), u[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+                        }
+                        *reinterpret_cast<uint4*>(dst + c) = make_uint4(u[0], u[1], u[2], u[3]);
+                        *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+                    }
+                }
+                soft_sync();  // the flag is free
+            }
+        }
+    } else if (warp < kSoftWarps + kDqWarps) {
+        const int id = threadIdx.x - kSoftWarps * 32;  // 0 .. 127
+        constexpr int KW = D / 8, VW = 16;             // words of codes: a token's K; V of 8 tokens x 16 values
+        const int vblk = id >> 4, vch = id & 15;       // V: this thread's 16 values, and 8 tokens
+        const bool vuse = vblk < D / 16;
+        uint32_t kc[KW], ks[D / 64], vc[VW], vs[2];
+        bool kbad = false;
+        // the group that holds a token of the item, or NULL: behind the end, or a bad page
+        auto find = [&](const Item& it, int tok, bool& badpage) -> const uint8_t* {
+            badpage = false;
+            if (tok >= it.L) return nullptr;
+            const int page = __ldg(a.table + it.b * a.ldb + (tok >> a.cache.page_log));
+            if (page < 0 || page >= a.cache.n_pages) {
+                atomicOr(a.status, kStatusBad);
+                badpage = true;
+                return nullptr;
+            }
+            return group_ptr<D>(a.cache, page, it.h, tok & ((1 << a.cache.page_log) - 1));
+        };
+        auto load_k = [&](const Item& it, int tile) {
+            const int tok = tile * kTok + id;
+            const uint8_t* g = find(it, tok, kbad);
+#pragma unroll
+            for (int i = 0; i < KW; ++i) kc[i] = 0u;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) ks[i] = 0u;
+            if (g) {
+                const int r = tok & 15;
+#pragma unroll
+                for (int i = 0; i < KW / 4; ++i) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(g + r * (D / 2)) + i);
+                    kc[4 * i] = u.x, kc[4 * i + 1] = u.y, kc[4 * i + 2] = u.z, kc[4 * i + 3] = u.w;
+                }
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) ks[i] = __ldg(reinterpret_cast<const uint32_t*>(g + k_scale_off(D) + r * (D / 16)) + i);
+            }
+        };
+        auto load_v = [&](const Item& it, int tile) {
+            const int tok = tile * kTok + vch * 8;
+            bool b;
+            const uint8_t* g = vuse ? find(it, tok, b) : nullptr;
+#pragma unroll
+            for (int i = 0; i < VW; ++i) vc[i] = 0u;
+            vs[0] = vs[1] = 0u;
+            if (g) {
+                const int r = tok & 15;  // 0 or 8
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(g + v_code_off(D) + vblk * 128 + r * 8) + i);
+                    vc[4 * i] = u.x, vc[4 * i + 1] = u.y, vc[4 * i + 2] = u.z, vc[4 * i + 3] = u.w;
+                }
+                const uint2 u = __ldg(reinterpret_cast<const uint2*>(g + v_scale_off(D) + vblk * 16 + r));
+                // places behind the end hold anything: scale 0, so that 0 * value is 0
+                const int left = it.L - tok;
+                vs[0] = left >= 4 ? u.x : u.x & ((1u << (8 * left)) - 1u);
+                vs[1] = left >= 8 ? u.y : left <= 4 ? 0u : u.y & ((1u << (8 * (left - 4))) - 1u);
+            }
+        };
+        int k = 0;
+        auto next_item = [&](Item& to) {  // the next one that has tokens
+            while (k < rounds) {
+                to = item(k++);
+                if (to.b >= 0 && to.t1 > to.t0) return true;
+            }
+            return false;
+        };
+        Item it = {};
+        bool more = next_item(it);
+        int tile = it.t0, tiles = 0;
+        if (more) {
+            load_k(it, tile);
+            load_v(it, tile);
+        }
+        while (more) {
+            const int s = tiles & 1;
+            if (tiles >= 2 && !wait(&kfree[s], ((tiles >> 1) - 1) & 1)) break;
+            {
+                uint8_t* dst = kt + s * C::kKBytes + id * 128;
+#pragma unroll
+                for (int w = 0; w < KW; w += 2) {  // 16 values under one scale
+                    const uint32_t two = e4m3x2_to_f16x2((ks[w / 8] >> (8 * ((w / 2) & 3))) & 0xffu);
+                    const uint32_t f = __byte_perm(two, 0, 0x1010);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t h[4];
+                        e2m1x8(kc[w + u], h);
+                        const int ch = w + u;  // 8 values: a 16-byte piece
+                        *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kTok * 128) + (((ch & 7) ^ (id & 7)) << 4)) =
+                            make_uint4(hmul2(h[0], f), hmul2(h[1], f), hmul2(h[2], f), hmul2(h[3], f));
+                    }
+                }
+                if ((id & 15) == 0) bad[(tiles & 3) * 8 + (id >> 4)] = kbad ? 1 : 0;
+            }
+            fence_proxy_async_smem();
+            arrive(&kfull[s]);
+            // the codes after these are in flight from here on
+            Item nit = it;
+            int ntile = tile + 1;
+            const bool nmore = ntile < it.t1 || next_item(nit);
+            if (ntile >= it.t1) ntile = nit.t0;
+            if (nmore) load_k(nit, ntile);
+            if (tiles >= 2 && !wait(&vfree[s], ((tiles >> 1) - 1) & 1)) break;
+            if (vuse) {
+                uint8_t* dst = vt + s * C::kVBytes + (vch >> 3) * (D * 128);
+                uint32_t f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = e4m3x2_to_f16x2((vs[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {  // a word: 8 of the 16 values
+                    constexpr uint32_t lo = 0x0f0f0f0fu;
+                    uint32_t xe[4][4], xo[4][4];  // [token pair][byte]: the even values, the odd ones
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t p0 = vc[4 * i + w], p1 = vc[4 * i + 2 + w];
+                        e2m1x8((p0 & lo) | ((p1 << 4) & ~lo), xe[i]);
+                        e2m1x8(((p0 >> 4) & lo) | (p1 & ~lo), xo[i]);
+                    }
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const int d = vblk * 16 + w * 8 + 2 * b;
+                        *reinterpret_cast<uint4*>(dst + d * 128 + (((vch & 7) ^ (d & 7)) << 4)) =
+                            make_uint4(hmul2(xe[0][b], f[0]), hmul2(xe[1][b], f[1]), hmul2(xe[2][b], f[2]), hmul2(xe[3][b], f[3]));
+                        *reinterpret_cast<uint4*>(dst + (d + 1) * 128 + (((vch & 7) ^ ((d + 1) & 7)) << 4)) =
+                            make_uint4(hmul2(xo[0][b], f[0]), hmul2(xo[1][b], f[1]), hmul2(xo[2][b], f[2]), hmul2(xo[3][b], f[3]));
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            arrive(&vfull[s]);
+            if (nmore) load_v(nit, ntile);
+            it = nit;
+            tile = ntile;
+            more = nmore;
+            ++tiles;
+        }
+    } else if (lane == 0) {
+        const uint32_t idesc_s = (1u << 4) | ((uint32_t)(kTok >> 3) << 17) | ((128u >> 4) << 24);  // fp16 x fp16 -> fp32
+        const uint32_t idesc_o = (1u << 4) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
+        int tiles = 0, q_its[2] = {0, 0}, p_tiles[2] = {0, 0};
+        bool ok = true;
+        const uint32_t sq = smem_u32(qt), sk = smem_u32(kt), sv = smem_u32(vt);
+        auto scores = [&](int x, int s) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const uint32_t at = (i >> 2) * (128 * 128) + (i & 3) * 32;
+                mma_ss(tmem + x * 128, sdesc(sq + x * C::kQBytes + at), sdesc(sk + s * C::kKBytes + at), idesc_s, i > 0);
+            }
+            commit(&sfull[x]);
+        };
+        for (int k = 0; k < rounds && ok; ++k) {
+            const Item it = item(k);
+            if (it.b < 0 || it.t1 <= it.t0) continue;
+            const int cnt = it.t1 - it.t0, two = it.rows > 128 ? 2 : 1;
+            for (int x = 0; x < two && ok; ++x) {
+                ok = wait(&qfull[x], q_its[x] & 1);
+                ++q_its[x];
+            }
+            ok = ok && wait(&kfull[tiles & 1], (tiles >> 1) & 1);
+            if (!ok) break;
+            fence_after();
+            for (int x = 0; x < two; ++x) scores(x, tiles & 1);
+            commit(&kfree[tiles & 1]);
+            for (int j = 0; j < cnt && ok; ++j, ++tiles) {
+                const int s = tiles & 1, sn = (tiles + 1) & 1;
+                ok = wait(&vfull[s], (tiles >> 1) & 1);
+                for (int x = 0; x < two && ok; ++x) {
+                    ok = wait(&pfull[x], p_tiles[x] & 1);
+                    ++p_tiles[x];
+                    if (!ok) break;
+                    fence_after();
+#pragma unroll
+                    for (int i = 0; i < kTok / 16; ++i)
+                        mma_ts(tmem + 256 + x * D, tmem + x * 128 + i * 8, sdesc(sv + s * C::kVBytes + (i >> 2) * (D * 128) + (i & 3) * 32),
+                               idesc_o, j > 0 || i > 0);
+                    if (x == two - 1) commit(&vfree[s]);
+                    if (j + 1 < cnt) {
+                        if (x == 0) {
+                            ok = wait(&kfull[sn], ((tiles + 1) >> 1) & 1);
+                            if (!ok) break;
+                            fence_after();
+                        }
+                        scores(x, sn);
+                        if (x == two - 1) commit(&kfree[sn]);
+                    } else {
+                        commit(&ofull[x]);
+                    }
+                }
+            }
+        }
+        commit(mma_done);  // every tensor-core operation of this thread is done before the teardown
+        if (!mbar_wait_bounded(mma_done, 0)) atomicOr(a.status, 1u);
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+}  // namespace kv
+}  // namespace qlin
+
+using namespace qlin;
+
+// Bytes of the parts of shared units at most.
+extern "C" size_t qlin_attn_chunk_part_bytes(int D, int sms) { return (size_t)2 * sms * kv::ch::kRows * (D + 2) * 4; }
+
+template <int D>
+static cudaError_t launch_chunk(kv::AttnArgs a, int sms, cudaStream_t s) {
+    using C = kv::ch::Cfg<D>;
+    static bool set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64) return cudaErrorInvalidDevice;
+    if (!set[dev]) {
+        e = cudaFuncSetAttribute(kv::attn_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::smem(kv::ch::kMaxSeqs));
+        if (e != cudaSuccess) return e;
+        set[dev] = true;
+    }
+    kv::attn_chunk_kernel<D><<<sms, kv::ch::kThreads, C::smem(a.B), s>>>(a);
+    return cudaGetLastError();
+}
+
+extern "C" cudaError_t qlin_launch_attn_chunk(const kv::AttnArgs* a, int D, int sms, cudaStream_t s) {
+    return D == 128 ? launch_chunk<128>(*a, sms, s) : launch_chunk<64>(*a, sms, s);
+}

@@ -1,29 +1,14 @@
 // attn_kv4.cu -- attention of single tokens and prompt chunks over the paged NVFP4 cache:
 // out = softmax(scale * q K^T) V with K and V dequantized in the kernel.
 //
-// A warp per (query, query head): 32 tokens at a time, a token a lane, with the running maximum and sum of the
-// softmax; the probabilities then go round the warp while each lane sums its D / 32 values of V.
+// Here: few query rows of a kv head (single tokens and a few more), and the choice between this kernel and the one for
+// prompt chunks (attn_chunk.cu).
 #include <cuda/std/type_traits>
 
-#include "kv_cache.cuh"
+#include "attn_common.cuh"
 
 namespace qlin {
 namespace kv {
-
-struct AttnArgs {
-    Cache cache;
-    const __nv_bfloat16* q;
-    __nv_bfloat16* out;
-    const int32_t *table, *lens, *cu;
-    int64_t ldq, ldo, ldb, total_q;
-    int max_pages, B, max_q, Hq, G;
-    float scale_log2;  // scale * k_scale * log2(e)
-    int window;        // 0: none; below 2^30
-    unsigned* status;
-    int RB, min_tiles;  // few rows: row blocks of a (sequence, head); fewest tiles that another CTA is worth
-    int* tickets;       // in the workspace: kMaxParts, zero between calls
-    float* parts;       // then two parts a CTA: rows x D sums, rows {maximum, sum}
-};
 
 // ------------------------------------------------------------------------------------- few rows, a long axis
 //
@@ -55,39 +40,12 @@ struct Dec {
     static constexpr int kFixed = kRing + kWarps * kStages * 16 + kWarps * 8 * 8 + kWarps * 32 * 4 + 2 * kQBytes + 16;
     static constexpr int smem(int B) { return kFixed + (3 * B + 2) * 4; }
 };
-constexpr int kMaxParts = 512;  // CTAs of a launch at most: tickets in the workspace
+constexpr int kFewRows = 64;      // rows of one (sequence, kv head) that this kernel takes at most
 constexpr int kMaxDecSeqs = 256;  // sequences of a launch
 static_assert(Dec<128, 1>::smem(kMaxDecSeqs) <= 232448 && Dec<64, 1>::smem(kMaxDecSeqs) <= 232448 &&
                   Dec<128, 2>::smem(kMaxDecSeqs) <= 232448 && Dec<64, 2>::smem(kMaxDecSeqs) <= 232448,
               "shared memory");
 static_assert(8 * Dec<128, 1>::kPad * 4 <= Dec<128, 1>::kStageBytes, "a warp's O of 8 rows fits a stage");
-
-// The tile of the first place that the first of a sequence's n queries sees.
-template <int TILE>
-__device__ __forceinline__ int first_tile(const AttnArgs& a, int n, int L) {
-    const int lo = a.window > 0 ? L - n + 1 - a.window : 0;
-    return lo > 0 ? lo / TILE : 0;
-}
-// A sequence's queries, context and tiles; bad ones have none.
-struct Seq {
-    int64_t row0;
-    int n, L, per;
-    bool bad;
-};
-template <int TILE>
-__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
-    Seq s;
-    s.row0 = __ldg(a.cu + b);
-    s.n = __ldg(a.cu + b + 1) - (int)s.row0;
-    s.L = __ldg(a.lens + b);
-    s.bad = s.n < 0 || s.n > a.max_q || s.row0 < 0 || s.row0 + s.n > a.total_q || s.L < 0 ||
-            (int64_t)s.L > ((int64_t)a.max_pages << a.cache.page_log);
-    s.per = 0;
-    if (!s.bad && s.n > 0 && s.L > 0) {
-        s.per = (s.L + TILE - 1) / TILE - first_tile<TILE>(a, s.n, s.L);
-    }
-    return s;
-}
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -100,34 +58,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-// The four f16x2 values of a word's bytes (low half: the byte's low nibble).
-__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
-    asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n cvt.rn.f16x2.e2m1x2 %0, b0;\n"
-        " cvt.rn.f16x2.e2m1x2 %1, b1;\n cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
-}
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
-    return r;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // A place in the list of tiles: tile i of (sequence b, head and row block hr).
 struct Cursor {
     int b, hr, i, per;
@@ -156,8 +86,8 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
             const int b = b0 + lane;
             int v = 0;
             if (b < a.B) {
-                const Seq s = seq_of<TILE>(a, b);
-                v = s.per;
+                const Seq s = seq_of(a, b);
+                if (!s.bad && s.n > 0 && s.L > 0) v = (s.L + TILE - 1) / TILE - first_tile<TILE>(a, s.n, s.L);
                 row0[b + 1] = (int)s.row0 + s.n, length[b] = s.L;
                 if (s.bad && blockIdx.x == 0) atomicOr(a.status, kStatusBad);
             }
@@ -177,7 +107,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
     // queries that see nothing at all: rows of zeros
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (prefix[b + 1] > prefix[b]) continue;
-        const Seq s = seq_of<TILE>(a, b);
+        const Seq s = seq_of(a, b);
         if (s.bad) continue;
         for (int64_t i = threadIdx.x; i < (int64_t)s.n * a.Hq * D / 8; i += W * 32) {
             const int64_t r = i / (a.Hq * D / 8), c = i % (a.Hq * D / 8);
@@ -265,9 +195,8 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
     int64_t s0 = t0 - seg.i;  // the first tile of this (sequence, head, row block)
     int done = 0;
     bool failed = false;
-    // The queries of a segment go to shared memory as fp16, scaled by a power of two (with the sign of the scale) that
-    // puts the row's largest magnitude in [2^14, 2^15): exact but for values 2^28 below it.  A row's D / 8 lanes hold 8
-    // values each; lane (g, t) of a product later reads its values (D / 4) t + 8 w .. + 7 of row g as one 16 bytes.
+    // The queries of a segment go to shared memory as fp16 (row_exponent).  A row's D / 8 lanes hold 8 values each; lane
+    // (g, t) of a product later reads its values (D / 4) t + 8 w .. + 7 of row g as one 16 bytes.
     constexpr int LPR = D / 8;
     const int qr = threadIdx.x / LPR, qd = threadIdx.x % LPR * 8;
     auto load_q = [&](const Cursor& c) {
@@ -283,22 +212,17 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         const uint32_t raw[4] = {u.x, u.y, u.z, u.w};
         float mx = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(raw[k] << 16)), fabsf(__uint_as_float(raw[k] & 0xffff0000u))));
+        for (int k = 0; k < 4; ++k) mx = fmaxf(mx, amax_bf16x2(raw[k]));
 #pragma unroll
         for (int k = LPR / 2; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-        // exponent of the largest magnitude, kept where both 2^(14 - e) and 2^(e - 14) are normal numbers
-        const int e = max(min((int)(__float_as_uint(mx) >> 23) - 127, 126), -100);
-        const float up = copysignf(__uint_as_float((uint32_t)(14 - e + 127) << 23), a.scale_log2);
+        const int e = row_exponent(mx);
+        const float up = row_up(e, a.scale_log2);
         uint32_t h[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            h[k] = pack_f16x2(__uint_as_float(raw[k] << 16) * up, __uint_as_float(raw[k] & 0xffff0000u) * up);
+        for (int k = 0; k < 4; ++k) h[k] = scaled_f16x2(raw[k], up);
         const int at = ((qd % (D / 4) / 8 * C::kRows + qr) * 4 + qd / (D / 4)) * 16;
         *reinterpret_cast<uint4*>(to + at) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (qd == 0)
-            reinterpret_cast<float*>(to + C::kRows * D * 2)[qr] =
-                fabsf(a.scale_log2) * __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+        if (qd == 0) reinterpret_cast<float*>(to + C::kRows * D * 2)[qr] = row_down(e, a.scale_log2);
     };
     uint4 qnext = load_q(seg);  // in flight with the first copies
     // one stage stays free: the last one read, which holds the warp's O while the warps' parts are joined
@@ -690,91 +614,13 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) attn_simple_kernel(const AttnArgs a) {
-    constexpr int V = D / 32;
-    __shared__ float qs[4][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.y * 4 + warp, b = blockIdx.z, i = blockIdx.x;
-    if (h >= a.Hq) return;
-    const int64_t r0 = a.cu[b];
-    const int n = a.cu[b + 1] - a.cu[b], L = a.lens[b];
-    if (n < 0 || n > a.max_q || r0 < 0 || r0 + n > a.total_q || L < 0 ||
-        (int64_t)L > ((int64_t)a.max_pages << a.cache.page_log)) {
-        if (lane == 0) atomicOr(a.status, kStatusBad);
-        return;
-    }
-    if (i >= n) return;
-    const int p = L - n + i, kvh = h / a.G;
-    const __nv_bfloat16* qr = a.q + (r0 + i) * a.ldq + (int64_t)h * D;
-    for (int d = lane; d < D; d += 32) qs[warp][d] = __bfloat162float(qr[d]) * a.scale_log2;
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, o[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) o[j] = 0.f;
-    const int first = a.window > 0 && p - a.window + 1 > 0 ? p - a.window + 1 : 0;
-    for (int t0 = first & ~15; t0 <= p; t0 += 32) {
-        const int t = t0 + lane;
-        float s = -INFINITY;
-        const uint8_t* g = nullptr;
-        if (t >= first && t <= p) {
-            const int page = a.table[b * a.ldb + (t >> a.cache.page_log)];
-            if (page < 0 || page >= a.cache.n_pages) {
-                atomicOr(a.status, kStatusBad);
-            } else {
-                g = group_ptr<D>(a.cache, page, kvh, t & ((1 << a.cache.page_log) - 1));
-                const int r = t & 15;
-                s = 0.f;
-                for (int blk = 0; blk < D / 16; ++blk) {
-                    const uint2 w = *reinterpret_cast<const uint2*>(g + r * (D / 2) + blk * 8);
-                    float x = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t c = e2m1x2_to_f16x2((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
-                        x += fp16_bits_to_f32(c & 0xffffu) * qs[warp][blk * 16 + 2 * j];
-                        x += fp16_bits_to_f32(c >> 16) * qs[warp][blk * 16 + 2 * j + 1];
-                    }
-                    s += x * e4m3_to_f32(g[k_scale_off(D) + r * (D / 16) + blk]);
-                }
-            }
-        }
-        float mx = s;
-#pragma unroll
-        for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-        const float mn = fmaxf(m, mx);
-        if (mn == -INFINITY) continue;
-        const float f = exp2f(m - mn), e = exp2f(s - mn);
-        m = mn;
-        l = l * f + e;
-#pragma unroll
-        for (int j = 0; j < V; ++j) o[j] *= f;
-        const unsigned long long gp = (unsigned long long)g;
-        for (int k = 0; k < 32; ++k) {
-            const float pe = __shfl_sync(0xffffffffu, e, k);
-            const uint8_t* gk = (const uint8_t*)__shfl_sync(0xffffffffu, gp, k);
-            if (gk == nullptr) continue;
-            const int r = (t0 + k) & 15, d = lane * V;
-            const float sc = pe * e4m3_to_f32(gk[v_scale_off(D) + (d >> 4) * 16 + r]);
-#pragma unroll
-            for (int j = 0; j < V; j += 2) {
-                const uint32_t c = e2m1x2_to_f16x2(gk[v_code_off(D) + (d >> 4) * 128 + r * 8 + ((d & 15) + j) / 2]);
-                o[j] += sc * fp16_bits_to_f32(c & 0xffffu);
-                o[j + 1] += sc * fp16_bits_to_f32(c >> 16);
-            }
-        }
-    }
-#pragma unroll
-    for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-    const float inv = l > 0.f ? a.cache.v_scale / l : 0.f;
-    __nv_bfloat16* orow = a.out + (r0 + i) * a.ldo + (int64_t)h * D + lane * V;
-#pragma unroll
-    for (int j = 0; j < V; ++j) orow[j] = __float2bfloat16_rn(o[j] * inv);
-}
-
 }  // namespace kv
 }  // namespace qlin
 
 using namespace qlin;
+
+extern "C" size_t qlin_attn_chunk_part_bytes(int D, int sms);
+extern "C" cudaError_t qlin_launch_attn_chunk(const kv::AttnArgs* a, int D, int sms, cudaStream_t s);
 
 static int kv_sm_count() {
     static int cached[64] = {};
@@ -790,8 +636,10 @@ static int kv_sm_count() {
 
 extern "C" size_t qlin_attn_kv4_ws_bytes(const qlin_kv_cache* c, int B, int max_q, int Hq) {
     (void)B;
-    const int rows = max_q * (Hq / c->Hkv) <= 8 ? 8 : 16;
-    return 256 + kv::kMaxParts * 4 + (size_t)2 * kv_sm_count() * rows * (c->D + 2) * 4;
+    const int64_t rows = (int64_t)max_q * (Hq / c->Hkv);
+    const size_t fixed = 256 + kv::kMaxParts * 4;
+    if (rows > kv::kFewRows) return fixed + qlin_attn_chunk_part_bytes(c->D, kv_sm_count());
+    return fixed + (size_t)2 * kv_sm_count() * (rows <= 8 ? 8 : 16) * (c->D + 2) * 4;
 }
 
 template <int D, int NT>
@@ -835,15 +683,8 @@ extern "C" cudaError_t qlin_launch_attn_kv4(const qlin_kv_cache* c, const void* 
     a.parts = (float*)((uint8_t*)ws + 256 + kv::kMaxParts * 4);
     a.min_tiles = 8;
     const int64_t rows = (int64_t)max_q * a.G;
-    if (rows <= 64) {
-        a.RB = rows <= 8 ? 1 : (int)((rows + 15) / 16);
-        if (c->D == 128) return rows <= 8 ? launch_decode<128, 1>(a, s) : launch_decode<128, 2>(a, s);
-        return rows <= 8 ? launch_decode<64, 1>(a, s) : launch_decode<64, 2>(a, s);
-    }
-    const dim3 grid((unsigned)max_q, (unsigned)((Hq + 3) / 4), (unsigned)B);
-    if (c->D == 128)
-        kv::attn_simple_kernel<128><<<grid, 128, 0, s>>>(a);
-    else
-        kv::attn_simple_kernel<64><<<grid, 128, 0, s>>>(a);
-    return cudaGetLastError();
+    if (rows > kv::kFewRows) return qlin_launch_attn_chunk(&a, c->D, kv_sm_count(), s);
+    a.RB = rows <= 8 ? 1 : (int)((rows + 15) / 16);
+    if (c->D == 128) return rows <= 8 ? launch_decode<128, 1>(a, s) : launch_decode<128, 2>(a, s);
+    return rows <= 8 ? launch_decode<64, 1>(a, s) : launch_decode<64, 2>(a, s);
 }
