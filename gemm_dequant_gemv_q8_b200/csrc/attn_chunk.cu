@@ -4,14 +4,15 @@
 // group size fills the tiles and K and V are dequantized once for all heads that share them.  A CTA (one an SM) works
 // on a unit's two tiles of 128 rows against 128 tokens at a time, tcgen05.mma kind::f16 with fp32 accumulators in tensor
 // memory:
-//   warps 0-3, 4-7: softmax of tile A and of tile B, a row a thread: scores from tensor memory, exponentials,
-//                   probabilities back as the fp16 A operand of P V (in the scores' columns); they also bring the
-//                   queries in (fp16, row_exponent) and take O out;
-//   warps 8-11    : dequantize K ([token][value], a token a thread) and V (transposed, [value][token], 16 values x 8
-//                   tokens a thread) into 128-byte-swizzled K-major tiles, two stages each, the next tile's codes
-//                   already in registers;
-//   warp 12       : one thread issues the products, S_A, S_B, then per tile of tokens P V of A, the next S_A, P V of B, the
-//                   next S_B: the tensor cores work for one tile while the other's softmax runs.
+//   warps 0-3, 4-7: softmax of tile A and of tile B, a row a thread: scores from tensor memory, once for their maximum
+//                   and once for the exponentials, probabilities back as the fp16 A operand of P V (in the scores'
+//                   columns); they also bring the queries in (fp16, row_exponent) and take O out;
+//   warps 8-11    : dequantize K, a token a thread, into a 128-byte-swizzled K-major tile [token][value];
+//   warps 12-15   : dequantize V into [value][token], 16 values x 8 tokens a thread; both in two stages, with the next
+//                   tile's codes on their way into registers and the page after that looked up;
+//   warp 16       : one thread issues the products: S_A, S_B, then per tile of tokens P V of A, the next S_A, P V of B, the
+//                   next S_B, so that the tensor cores work for one tile while the other's softmax runs
+//                   (warps 17-19 are idle: registers are dealt out by four warps).
 // The exponent's reference follows the running maximum only when that has grown by 2^8, so O is rarely rescaled.
 // Units are dealt out heaviest first, there and back; those of the last, partial round are split along the tokens
 // where that shortens it, and the last CTA of a unit to finish joins its parts in their order.
@@ -26,8 +27,11 @@ namespace kv {
 namespace ch {
 
 constexpr int kRows = 256, kTok = 128;
-constexpr int kSoftWarps = 8, kDqWarps = 4;
-constexpr int kThreads = (kSoftWarps + kDqWarps + 1) * 32;
+constexpr int kSoftWarps = 8, kDqWarps = 4, kMmaWarp = kSoftWarps + 2 * kDqWarps;
+constexpr int kThreads = (kMmaWarp + 4) * 32;
+// Registers a thread: 96 at launch (640 threads), then by role; the softmax warps' share comes from the others'.
+constexpr int kSoftRegs = 120, kDqRegs = 80, kMmaRegs = 72;
+static_assert(256 * kSoftRegs + 256 * kDqRegs + 128 * kMmaRegs <= 640 * 96, "the launch's registers");
 constexpr int kMaxSeqs = 1024;
 constexpr int kSplitCost = 3;  // tiles that a split's queries, rows and joining cost
 
@@ -68,8 +72,7 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 __device__ __forceinline__ void arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void ld32(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
+__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {  // complete after ld_wait
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -78,10 +81,8 @@ __device__ __forceinline__ void ld32(uint32_t taddr, float (&v)[32]) {
           "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -90,6 +91,13 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
         "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
         "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
         : "memory");
 }
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -143,7 +151,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
         *tail_tiles = 0;
         fence_mbar_init();
     }
-    if (warp == 12) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_holder)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
@@ -242,6 +250,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
     };
 
     if (warp < kSoftWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int x = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane, srow = x * 128 + row;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + 256 + x * D;
@@ -266,29 +275,24 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             const bool active = x * 128 < it.rows && cnt > 0 && ok;
             if (active) {
                 // queries: the row as fp16, 16-byte pieces of 128-byte rows turned by the row
-                uint32_t w[D / 2];
                 float mx = 0.f;
+                const uint4* src = reinterpret_cast<const uint4*>(a.q + qrow * a.ldq + (int64_t)head * D);
                 if (valid) {
-                    const uint4* src = reinterpret_cast<const uint4*>(a.q + qrow * a.ldq + (int64_t)head * D);
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i) {
                         const uint4 u = __ldg(src + i);
-                        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+                        mx = fmaxf(mx, fmaxf(fmaxf(amax_bf16x2(u.x), amax_bf16x2(u.y)), fmaxf(amax_bf16x2(u.z), amax_bf16x2(u.w))));
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < D / 2; ++i) w[i] = 0u;
                 }
-#pragma unroll
-                for (int i = 0; i < D / 2; ++i) mx = fmaxf(mx, amax_bf16x2(w[i]));
                 const int e = row_exponent(mx);
                 const float up = row_up(e, a.scale_log2);
                 rs = row_down(e, a.scale_log2);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i)
+#pragma unroll 4
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 u = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
                     *reinterpret_cast<uint4*>(qx + (i >> 3) * (128 * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
-                        make_uint4(scaled_f16x2(w[4 * i], up), scaled_f16x2(w[4 * i + 1], up),
-                                   scaled_f16x2(w[4 * i + 2], up), scaled_f16x2(w[4 * i + 3], up));
+                        make_uint4(scaled_f16x2(u.x, up), scaled_f16x2(u.y, up), scaled_f16x2(u.z, up), scaled_f16x2(u.w, up));
+                }
                 fence_proxy_async_smem();
                 arrive(&qfull[x]);
                 for (int j = 0; j < cnt; ++j) {
@@ -299,87 +303,91 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                     const int tok0 = (it.t0 + j) * kTok;
                     const uint64_t out = *reinterpret_cast<const volatile uint64_t*>(bad + ((all_tiles + j) & 3) * 8);
                     const bool edge = out != 0 || tok0 + kTok - 1 > pw0 || (a.window > 0 && tok0 <= pw1 - a.window);
-                    uint32_t pk[64];
-                    // one pass with the reference as it is; a second one where a score is more than 2^8 above it
-                    auto pass = [&](auto masked, auto only_max, float ref) {
-                        float top = -INFINITY;
-                        float2 sum = make_float2(0.f, 0.f);
-                        const float2 rs2 = make_float2(rs, rs), ref2 = make_float2(-ref, -ref);
+                    auto sees = [&](int i) {  // whether this row sees the tile's token i
+                        const int tk = tok0 + i;
+                        return tk <= p && (a.window == 0 || tk > p - a.window) && !((out >> (8 * (i >> 4))) & 1);
+                    };
+                    auto load = [&](int c, float (&v)[32]) {  // 32 of the tile's scores
+                        uint32_t u[32];
+                        ld32(ts + 32 * c, u);
+                        ld_wait();
 #pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+                    };
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32], t0 = -INFINITY, t1 = -INFINITY;
+                        load(c, v);
+                        if (edge) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = sees(32 * c + i) ? v[i] : -INFINITY;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            t0 = fmaxf(t0, fmaxf(v[i], v[i + 1]));
+                            t1 = fmaxf(t1, fmaxf(v[i + 2], v[i + 3]));
+                        }
+                        top = fmaxf(top, fmaxf(t0, t1));
+                    }
+                    top = top == -INFINITY ? top : __fmul_rn(top, rs);
+                    if (__any_sync(0xffffffffu, top > m + 8.f)) {
+                        const float mn = fmaxf(m, top);
+                        const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+                        m = mn;
+                        l *= f;
+                        if (j > 0) {  // the products before this tile are done: S of this tile came after them
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t u[32];
+                                ld32(to + c, u);
+                                ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
+                                st32(to + c, u);
+                            }
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    float2 sum = make_float2(0.f, 0.f);
+                    // the probabilities go where scores have been read already
+                    if (edge || __any_sync(0xffffffffu, fabsf(ref) >= 0x1p24f)) {
+                        // The careful form rounds twice, as the reference does: the largest score's exponent is 0 whatever
+                        // its size.  One rounding (below) leaves up to half an ulp of the reference there, less than 1
+                        // below 2^24, the same for the whole row.
+#pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             float v[32];
-                            ld32(ts + 32 * c, v);
-                            if constexpr (decltype(masked)::value) {
+                            load(c, v);
+                            uint32_t pk[16];
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) {
-                                    const int tk = tok0 + 32 * c + i;
-                                    const bool sees = tk <= p && (a.window == 0 || tk > p - a.window) &&
-                                                      !((out >> (8 * ((32 * c + i) >> 4))) & 1);
-                                    v[i] = sees ? v[i] : -INFINITY;
-                                }
+                            for (int i = 0; i < 32; i += 2) {
+                                float2 e2 = make_float2(ex2(__fsub_rn(__fmul_rn(v[i], rs), ref)), ex2(__fsub_rn(__fmul_rn(v[i + 1], rs), ref)));
+                                e2.x = sees(32 * c + i) ? e2.x : 0.f;
+                                e2.y = sees(32 * c + i + 1) ? e2.y : 0.f;
+                                sum = __fadd2_rn(sum, e2);
+                                pk[i / 2] = pack_f16x2(e2.x, e2.y);
                             }
-                            float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                t0 = fmaxf(t0, fmaxf(v[i], v[i + 1]));
-                                t1 = fmaxf(t1, fmaxf(v[i + 2], v[i + 3]));
-                            }
-                            top = fmaxf(top, fmaxf(t0, t1));
-                            if constexpr (!decltype(only_max)::value) {
-#pragma unroll
-                                for (int i = 0; i < 32; i += 2) {
-                                    // The careful form rounds twice, as the reference does: the largest score's exponent
-                                    // is 0 whatever its size.  One rounding leaves up to half an ulp of the reference there,
-                                    // less than 1 below 2^24, the same for the whole row.
-                                    float2 y;
-                                    if constexpr (decltype(masked)::value)
-                                        y = make_float2(__fsub_rn(__fmul_rn(v[i], rs), ref), __fsub_rn(__fmul_rn(v[i + 1], rs), ref));
-                                    else
-                                        y = __ffma2_rn(make_float2(v[i], v[i + 1]), rs2, ref2);
-                                    float2 e2 = make_float2(ex2(y.x), ex2(y.y));
-                                    if constexpr (decltype(masked)::value) {  // also where rs is 0
-                                        e2.x = v[i] == -INFINITY ? 0.f : e2.x;
-                                        e2.y = v[i + 1] == -INFINITY ? 0.f : e2.y;
-                                    }
-                                    sum = __fadd2_rn(sum, e2);
-                                    pk[16 * c + i / 2] = pack_f16x2(e2.x, e2.y);
-                                }
-                            }
+                            st16(ts + 16 * c, pk);
                         }
-                        return make_float2(top == -INFINITY ? top : __fmul_rn(top, rs), sum.x + sum.y);
-                    };
-                    const cuda::std::true_type yes;
-                    const cuda::std::false_type no;
-                    float2 got;
-                    bool again = __any_sync(0xffffffffu, m == -INFINITY);
-                    for (;;) {
-                        if (again) {
-                            const float top = edge ? pass(yes, yes, 0.f).x : pass(no, yes, 0.f).x;
-                            const float mn = fmaxf(m, top);
-                            const float f = m == -INFINITY ? 0.f : ex2(m - mn);
-                            m = mn;
-                            l *= f;
-                            if (j > 0) {  // the products before this tile are done: S of this tile came after them
+                    } else {
+                        const float2 rs2 = make_float2(rs, rs), ref2 = make_float2(-ref, -ref);
 #pragma unroll 1
-                                for (int c = 0; c < D; c += 32) {
-                                    float v[32];
-                                    ld32(to + c, v);
-                                    uint32_t u[32];
+                        for (int c = 0; c < 4; ++c) {
+                            float v[32];
+                            load(c, v);
+                            uint32_t pk[16];
 #pragma unroll
-                                    for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * f);
-                                    st32(to + c, u);
-                                }
+                            for (int i = 0; i < 32; i += 2) {
+                                const float2 y = __ffma2_rn(make_float2(v[i], v[i + 1]), rs2, ref2);
+                                const float2 e2 = make_float2(ex2(y.x), ex2(y.y));
+                                sum = __fadd2_rn(sum, e2);
+                                pk[i / 2] = pack_f16x2(e2.x, e2.y);
                             }
+                            st16(ts + 16 * c, pk);
                         }
-                        const float ref = m == -INFINITY ? 0.f : m;
-                        const bool careful = edge || __any_sync(0xffffffffu, fabsf(ref) >= 0x1p24f);
-                        got = careful ? pass(yes, no, ref) : pass(no, no, ref);
-                        if (again || !__any_sync(0xffffffffu, got.x > m + 8.f)) break;
-                        again = true;
                     }
-                    l += got.y;
-                    st32(ts, pk);
-                    st32(ts + 32, pk + 32);
+                    l += sum.x + sum.y;
                     st_wait();
                     fence_before();
                     arrive(&pfull[x]);
@@ -397,12 +405,16 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float v[32];
+                uint32_t raw[32];
                 if (active && ok) {
-                    ld32(to + c, v);
+                    ld32(to + c, raw);
+                    ld_wait();
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                    for (int i = 0; i < 32; ++i) raw[i] = 0u;
                 }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
                 if (!valid) continue;
                 if (it.parts == 1) {
 #pragma unroll
@@ -471,64 +483,15 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                 soft_sync();  // the flag is free
             }
         }
-    } else if (warp < kSoftWarps + kDqWarps) {
-        const int id = threadIdx.x - kSoftWarps * 32;  // 0 .. 127
-        constexpr int KW = D / 8, VW = 16;             // words of codes: a token's K; V of 8 tokens x 16 values
-        const int vblk = id >> 4, vch = id & 15;       // V: this thread's 16 values, and 8 tokens
-        const bool vuse = vblk < D / 16;
-        uint32_t kc[KW], ks[D / 64], vc[VW], vs[2];
-        bool kbad = false;
-        // the group that holds a token of the item, or NULL: behind the end, or a bad page
-        auto find = [&](const Item& it, int tok, bool& badpage) -> const uint8_t* {
-            badpage = false;
-            if (tok >= it.L) return nullptr;
-            const int page = __ldg(a.table + it.b * a.ldb + (tok >> a.cache.page_log));
-            if (page < 0 || page >= a.cache.n_pages) {
-                atomicOr(a.status, kStatusBad);
-                badpage = true;
-                return nullptr;
-            }
-            return group_ptr<D>(a.cache, page, it.h, tok & ((1 << a.cache.page_log) - 1));
-        };
-        auto load_k = [&](const Item& it, int tile) {
-            const int tok = tile * kTok + id;
-            const uint8_t* g = find(it, tok, kbad);
-#pragma unroll
-            for (int i = 0; i < KW; ++i) kc[i] = 0u;
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) ks[i] = 0u;
-            if (g) {
-                const int r = tok & 15;
-#pragma unroll
-                for (int i = 0; i < KW / 4; ++i) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(g + r * (D / 2)) + i);
-                    kc[4 * i] = u.x, kc[4 * i + 1] = u.y, kc[4 * i + 2] = u.z, kc[4 * i + 3] = u.w;
-                }
-#pragma unroll
-                for (int i = 0; i < D / 64; ++i) ks[i] = __ldg(reinterpret_cast<const uint32_t*>(g + k_scale_off(D) + r * (D / 16)) + i);
-            }
-        };
-        auto load_v = [&](const Item& it, int tile) {
-            const int tok = tile * kTok + vch * 8;
-            bool b;
-            const uint8_t* g = vuse ? find(it, tok, b) : nullptr;
-#pragma unroll
-            for (int i = 0; i < VW; ++i) vc[i] = 0u;
-            vs[0] = vs[1] = 0u;
-            if (g) {
-                const int r = tok & 15;  // 0 or 8
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(g + v_code_off(D) + vblk * 128 + r * 8) + i);
-                    vc[4 * i] = u.x, vc[4 * i + 1] = u.y, vc[4 * i + 2] = u.z, vc[4 * i + 3] = u.w;
-                }
-                const uint2 u = __ldg(reinterpret_cast<const uint2*>(g + v_scale_off(D) + vblk * 16 + r));
-                // places behind the end hold anything: scale 0, so that 0 * value is 0
-                const int left = it.L - tok;
-                vs[0] = left >= 4 ? u.x : u.x & ((1u << (8 * left)) - 1u);
-                vs[1] = left >= 8 ? u.y : left <= 4 ? 0u : u.y & ((1u << (8 * (left - 4))) - 1u);
-            }
-        };
+    } else if (warp < kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDqRegs));
+        const bool isv = warp >= kSoftWarps + kDqWarps;
+        const int id = threadIdx.x - (isv ? kSoftWarps + kDqWarps : kSoftWarps) * 32;  // 0 .. 127
+        // K: token id of the tile.  V: 16 values, block id / 16, of 8 tokens from 8 (id % 16)
+        const int vblk = id >> 4, vch = id & 15, at = isv ? vch * 8 : id;
+        const bool use = !isv || vblk < D / 16;
+        constexpr int CW = 16;                 // words of codes a thread at most
+        constexpr int KW = D / 8, KS = D / 64;  // words of codes and of scales of a token's K
         int k = 0;
         auto next_item = [&](Item& to) {  // the next one that has tokens
             while (k < rounds) {
@@ -537,76 +500,124 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             }
             return false;
         };
+        // a tile that this thread has looked up: the group of its token, or NULL (behind the end, a bad page)
+        struct Place {
+            const uint8_t* g;
+            int left;  // tokens from this thread's to the context's end
+            bool bad;
+        };
         Item it = {};
-        bool more = next_item(it);
-        int tile = it.t0, tiles = 0;
-        if (more) {
-            load_k(it, tile);
-            load_v(it, tile);
-        }
-        while (more) {
+        int tile = 0;
+        bool more = true;
+        auto step = [&]() {  // on to the next tile, its page looked up
+            Place pl = {nullptr, 0, false};
+            if (more && ++tile >= it.t1) {
+                more = next_item(it);
+                tile = it.t0;
+            }
+            if (!more || !use) return pl;
+            const int tok = tile * kTok + at;
+            pl.left = it.L - tok;
+            if (pl.left <= 0) return pl;
+            const int page = __ldg(a.table + it.b * a.ldb + (tok >> a.cache.page_log));
+            if (page < 0 || page >= a.cache.n_pages) {
+                atomicOr(a.status, kStatusBad);
+                pl.bad = true;
+                return pl;
+            }
+            pl.g = group_ptr<D>(a.cache, page, it.h, tok & ((1 << a.cache.page_log) - 1));
+            return pl;
+        };
+        uint64_t *full = isv ? vfull : kfull, *free_ = isv ? vfree : kfree;
+        auto fetch = [&](const Place& pl, uint32_t (&c)[CW], uint32_t (&sc)[2]) {
+#pragma unroll
+            for (int i = 0; i < CW; ++i) c[i] = 0u;
+            sc[0] = sc[1] = 0u;
+            if (!pl.g) return;
+            const int r = at & 15;  // V: 0 or 8
+            const uint4* src = reinterpret_cast<const uint4*>(isv ? pl.g + v_code_off(D) + vblk * 128 + r * 8 : pl.g + r * (D / 2));
+            const uint32_t* ssrc =
+                reinterpret_cast<const uint32_t*>(isv ? pl.g + v_scale_off(D) + vblk * 16 + r : pl.g + k_scale_off(D) + r * (D / 16));
+#pragma unroll
+            for (int i = 0; i < CW / 4; ++i) {
+                if (i >= KW / 4 && !isv) break;
+                const uint4 u = __ldg(src + i);
+                c[4 * i] = u.x, c[4 * i + 1] = u.y, c[4 * i + 2] = u.z, c[4 * i + 3] = u.w;
+            }
+            sc[0] = __ldg(ssrc);
+            if (isv || KS > 1) sc[1] = __ldg(ssrc + 1);
+        };
+        uint32_t c[CW], sc[2];
+        Place now, next;
+        bool cur = next_item(it);  // whether `now` is a tile
+        more = cur;
+        tile = it.t0 - 1;
+        now = step();
+        fetch(now, c, sc);
+        bool nmore = cur;
+        next = step();
+        nmore = more;
+        for (int tiles = 0; cur; ++tiles) {
             const int s = tiles & 1;
-            if (tiles >= 2 && !wait(&kfree[s], ((tiles >> 1) - 1) & 1)) break;
-            {
+            uint32_t nc[CW], nsc[2];
+            fetch(next, nc, nsc);
+            const Place ahead = step();
+            const bool amore = more;
+            if (tiles >= 2 && !wait(&free_[s], ((tiles >> 1) - 1) & 1)) break;
+            if (!isv) {
                 uint8_t* dst = kt + s * C::kKBytes + id * 128;
 #pragma unroll
                 for (int w = 0; w < KW; w += 2) {  // 16 values under one scale
-                    const uint32_t two = e4m3x2_to_f16x2((ks[w / 8] >> (8 * ((w / 2) & 3))) & 0xffu);
+                    const uint32_t two = e4m3x2_to_f16x2((sc[w / 8] >> (8 * ((w / 2) & 3))) & 0xffu);
                     const uint32_t f = __byte_perm(two, 0, 0x1010);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         uint32_t h[4];
-                        e2m1x8(kc[w + u], h);
-                        const int ch = w + u;  // 8 values: a 16-byte piece
-                        *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kTok * 128) + (((ch & 7) ^ (id & 7)) << 4)) =
+                        e2m1x8(c[w + u], h);
+                        const int piece = w + u;  // 8 values: 16 bytes
+                        *reinterpret_cast<uint4*>(dst + (piece >> 3) * (kTok * 128) + (((piece & 7) ^ (id & 7)) << 4)) =
                             make_uint4(hmul2(h[0], f), hmul2(h[1], f), hmul2(h[2], f), hmul2(h[3], f));
                     }
                 }
-                if ((id & 15) == 0) bad[(tiles & 3) * 8 + (id >> 4)] = kbad ? 1 : 0;
-            }
-            fence_proxy_async_smem();
-            arrive(&kfull[s]);
-            // the codes after these are in flight from here on
-            Item nit = it;
-            int ntile = tile + 1;
-            const bool nmore = ntile < it.t1 || next_item(nit);
-            if (ntile >= it.t1) ntile = nit.t0;
-            if (nmore) load_k(nit, ntile);
-            if (tiles >= 2 && !wait(&vfree[s], ((tiles >> 1) - 1) & 1)) break;
-            if (vuse) {
+                if ((id & 15) == 0) bad[(tiles & 3) * 8 + (id >> 4)] = now.bad ? 1 : 0;
+            } else if (use) {
                 uint8_t* dst = vt + s * C::kVBytes + (vch >> 3) * (D * 128);
-                uint32_t f[4];
+                // places behind the end hold anything: scale 0, so that 0 * value is 0
+                const uint32_t s0 = now.left >= 4 ? sc[0] : now.left <= 0 ? 0u : sc[0] & ((1u << (8 * now.left)) - 1u);
+                const uint32_t s1 = now.left >= 8 ? sc[1] : now.left <= 4 ? 0u : sc[1] & ((1u << (8 * (now.left - 4))) - 1u);
+                const uint32_t f[4] = {e4m3x2_to_f16x2(s0 & 0xffffu), e4m3x2_to_f16x2(s0 >> 16), e4m3x2_to_f16x2(s1 & 0xffffu),
+                                       e4m3x2_to_f16x2(s1 >> 16)};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = e4m3x2_to_f16x2((vs[i >> 1] >> (16 * (i & 1))) & 0xffffu);
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {  // a word: 8 of the 16 values
+                for (int w = 0; w < 2; ++w) {  // a word of each token: 8 of the 16 values
                     constexpr uint32_t lo = 0x0f0f0f0fu;
-                    uint32_t xe[4][4], xo[4][4];  // [token pair][byte]: the even values, the odd ones
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t p0 = vc[4 * i + w], p1 = vc[4 * i + 2 + w];
-                        e2m1x8((p0 & lo) | ((p1 << 4) & ~lo), xe[i]);
-                        e2m1x8(((p0 >> 4) & lo) | (p1 & ~lo), xo[i]);
-                    }
+                    for (int odd = 0; odd < 2; ++odd) {  // the even values, then the odd ones
+                        uint32_t x[4][4];                // [token pair][byte]
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const int d = vblk * 16 + w * 8 + 2 * b;
-                        *reinterpret_cast<uint4*>(dst + d * 128 + (((vch & 7) ^ (d & 7)) << 4)) =
-                            make_uint4(hmul2(xe[0][b], f[0]), hmul2(xe[1][b], f[1]), hmul2(xe[2][b], f[2]), hmul2(xe[3][b], f[3]));
-                        *reinterpret_cast<uint4*>(dst + (d + 1) * 128 + (((vch & 7) ^ ((d + 1) & 7)) << 4)) =
-                            make_uint4(hmul2(xo[0][b], f[0]), hmul2(xo[1][b], f[1]), hmul2(xo[2][b], f[2]), hmul2(xo[3][b], f[3]));
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t p0 = c[4 * i + w], p1 = c[4 * i + 2 + w];
+                            e2m1x8(odd ? ((p0 >> 4) & lo) | (p1 & ~lo) : (p0 & lo) | ((p1 << 4) & ~lo), x[i]);
+                        }
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const int d = vblk * 16 + w * 8 + 2 * b + odd;
+                            *reinterpret_cast<uint4*>(dst + d * 128 + (((vch & 7) ^ (d & 7)) << 4)) =
+                                make_uint4(hmul2(x[0][b], f[0]), hmul2(x[1][b], f[1]), hmul2(x[2][b], f[2]), hmul2(x[3][b], f[3]));
+                        }
                     }
                 }
             }
             fence_proxy_async_smem();
-            arrive(&vfull[s]);
-            if (nmore) load_v(nit, ntile);
-            it = nit;
-            tile = ntile;
-            more = nmore;
-            ++tiles;
+            arrive(&full[s]);
+#pragma unroll
+            for (int i = 0; i < CW; ++i) c[i] = nc[i];
+            sc[0] = nsc[0], sc[1] = nsc[1];
+            now = next, next = ahead;
+            cur = nmore, nmore = amore;
         }
-    } else if (lane == 0) {
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+        if (warp == kMmaWarp && lane == 0) {
         const uint32_t idesc_s = (1u << 4) | ((uint32_t)(kTok >> 3) << 17) | ((128u >> 4) << 24);  // fp16 x fp16 -> fp32
         const uint32_t idesc_o = (1u << 4) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
         int tiles = 0, q_its[2] = {0, 0}, p_tiles[2] = {0, 0};
@@ -662,10 +673,11 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
         }
         commit(mma_done);  // every tensor-core operation of this thread is done before the teardown
         if (!mbar_wait_bounded(mma_done, 0)) atomicOr(a.status, 1u);
+        }
     }
     fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kMmaWarp) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
