@@ -7,12 +7,12 @@
 //   warps 0-3, 4-7: softmax of tile A and of tile B, a row a thread: scores from tensor memory, once for their maximum
 //                   and once for the exponentials, probabilities back as the fp16 A operand of P V (in the scores'
 //                   columns); they also bring the queries in (fp16, row_exponent) and take O out;
-//   warps 8-11    : dequantize K, a token a thread, into a 128-byte-swizzled K-major tile [token][value];
-//   warps 12-15   : dequantize V into [value][token], 16 values x 8 tokens a thread; both in two stages, with the next
-//                   tile's codes on their way into registers and the page after that looked up;
-//   warp 16       : one thread issues the products: S_A, S_B, then per tile of tokens P V of A, the next S_A, P V of B, the
+//   warps 8-11    : dequantize K, a token a thread, and V, 16 values x 8 tokens a thread, into 128-byte-swizzled K-major
+//                   tiles [token][value] and [value][token] in two stages each, with the next tile's codes on their way
+//                   into registers and the pages after that looked up;
+//   warp 12       : one thread issues the products: S_A, S_B, then per tile of tokens P V of A, the next S_A, P V of B, the
 //                   next S_B, so that the tensor cores work for one tile while the other's softmax runs
-//                   (warps 17-19 are idle: registers are dealt out by four warps).
+//                   (warps 13-15 are idle: registers are dealt out by four warps).
 // The exponent's reference follows the running maximum only when that has grown by 2^8, so O is rarely rescaled.
 // Units are dealt out heaviest first, there and back; those of the last, partial round are split along the tokens
 // where that shortens it, and the last CTA of a unit to finish joins its parts in their order.
@@ -27,11 +27,11 @@ namespace kv {
 namespace ch {
 
 constexpr int kRows = 256, kTok = 128;
-constexpr int kSoftWarps = 8, kDqWarps = 4, kMmaWarp = kSoftWarps + 2 * kDqWarps;
+constexpr int kSoftWarps = 8, kDqWarps = 4, kMmaWarp = kSoftWarps + kDqWarps;
 constexpr int kThreads = (kMmaWarp + 4) * 32;
-// Registers a thread: 96 at launch (640 threads), then by role; the softmax warps' share comes from the others'.
-constexpr int kSoftRegs = 120, kDqRegs = 80, kMmaRegs = 72;
-static_assert(256 * kSoftRegs + 256 * kDqRegs + 128 * kMmaRegs <= 640 * 96, "the launch's registers");
+// Registers a thread: 128 at launch (512 threads), then by role; the softmax warps' share comes from the idle ones'.
+constexpr int kSoftRegs = 152, kDqRegs = 128, kMmaRegs = 72;
+static_assert(256 * kSoftRegs + 128 * kDqRegs + 128 * kMmaRegs <= 512 * 128, "the launch's registers");
 constexpr int kMaxSeqs = 1024;
 constexpr int kSplitCost = 3;  // tiles that a split's queries, rows and joining cost
 
@@ -39,7 +39,7 @@ template <int D>
 struct Cfg {
     static constexpr int kQBytes = 128 * D * 2;  // one tile of queries
     static constexpr int kKBytes = kTok * D * 2, kVBytes = kTok * D * 2;
-    static constexpr int kSmem = 1024 + 2 * kQBytes + 2 * kKBytes + 2 * kVBytes + 512;
+    static constexpr int kSmem = 1024 + 2 * kQBytes + 2 * kKBytes + 2 * kVBytes + 512 + (kMmaWarp + 1) * 64;
     static constexpr int smem(int B) { return kSmem + (3 * B + 2) * 4; }
 };
 static_assert(Cfg<128>::smem(kMaxSeqs) <= 232448, "shared memory");
@@ -82,7 +82,14 @@ __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {  // complete
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
-__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The wait names the registers, so that nothing reads them before it.
+__device__ __forceinline__ void ld_wait(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
 __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -110,6 +117,7 @@ struct Item {
     int part, parts;  // part of a unit that several CTAs share (parts > 1)
     int tail;         // its number among the shared ones
 };
+static_assert(sizeof(Item) <= 64, "an item's slot");
 
 }  // namespace ch
 
@@ -130,7 +138,8 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     int* last_flag = reinterpret_cast<int*>(tmem_holder + 2);
     int* tail_tiles = reinterpret_cast<int*>(tmem_holder + 3);  // of all units of the last round
-    int* prefix = reinterpret_cast<int*>(bars + 64);      // [B + 1] units of one kv head before sequence b
+    Item* slots = reinterpret_cast<Item*>(bars + 64);     // [warp] the piece of work it is at
+    int* prefix = reinterpret_cast<int*>(slots + kMmaWarp + 1);  // [B + 1] units of one kv head before sequence b
     int *row0 = prefix + a.B + 1, *length = row0 + a.B + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int Hkv = a.cache.Hkv;
@@ -241,6 +250,13 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
         return it;
     };
     const int rounds = (items + grid - 1) / grid;
+    // A warp's k-th piece of work, in its slot: what a role does not need at the moment takes no register.
+    auto take = [&](int k) -> const Item& {
+        __syncwarp();
+        if (lane == 0) slots[warp] = item(k);
+        __syncwarp();
+        return slots[warp];
+    };
     auto wait = [&](uint64_t* bar, int parity) {  // false: gave up, or another warp has
         if (*abort_flag) return false;
         if (mbar_wait_bounded(bar, parity)) return true;
@@ -260,38 +276,44 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
         auto warp_wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
         int all_tiles = 0;       // of the CTA: the bad groups' ring
         for (int k = 0; k < rounds; ++k) {
-            const Item it = item(k);
+            const Item& it = take(k);
             if (it.b < 0) continue;
-            const int cnt = it.t1 - it.t0;
-            const int r = it.base + srow, tok = r / a.G;
-            const bool valid = srow < it.rows;
-            const int64_t qrow = it.row0 + tok;
-            const int head = it.h * a.G + r % a.G;
-            const int p = it.L - it.n + tok;  // the last place this row sees
+            const int cnt = it.t1 - it.t0, first = it.t0;
+            const int p = it.L - it.n + (it.base + srow) / a.G;  // the last place this row sees
             // of this warp's rows: the first one's and the last one's
             const int pw0 = it.L - it.n + (it.base + x * 128 + quarter * 32) / a.G;
             const int pw1 = it.L - it.n + (it.base + x * 128 + quarter * 32 + 31) / a.G;
             float rs = 0.f, m = -INFINITY, l = 0.f;
             const bool active = x * 128 < it.rows && cnt > 0 && ok;
             if (active) {
-                // queries: the row as fp16, 16-byte pieces of 128-byte rows turned by the row
-                float mx = 0.f;
-                const uint4* src = reinterpret_cast<const uint4*>(a.q + qrow * a.ldq + (int64_t)head * D);
-                if (valid) {
+                // This warp's 32 rows of queries as fp16, 16-byte pieces of 128-byte rows turned by the row: D / 8 lanes a row,
+                // so that a load is whole rows.
+                constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows a load
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 u = __ldg(src + i);
-                        mx = fmaxf(mx, fmaxf(fmaxf(amax_bf16x2(u.x), amax_bf16x2(u.y)), fmaxf(amax_bf16x2(u.z), amax_bf16x2(u.w))));
+                for (int h0 = 0; h0 < 32; h0 += 8 * RPI) {
+                    uint4 u[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int wr = quarter * 32 + h0 + i * RPI + lane / LPR, rr = it.base + x * 128 + wr;
+                        u[i] = make_uint4(0, 0, 0, 0);
+                        if (x * 128 + wr < it.rows)
+                            u[i] = __ldg(reinterpret_cast<const uint4*>(a.q + (it.row0 + rr / a.G) * a.ldq +
+                                                                        (int64_t)(it.h * a.G + rr % a.G) * D) + lane % LPR);
                     }
-                }
-                const int e = row_exponent(mx);
-                const float up = row_up(e, a.scale_log2);
-                rs = row_down(e, a.scale_log2);
-#pragma unroll 4
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 u = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(qx + (i >> 3) * (128 * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
-                        make_uint4(scaled_f16x2(u.x, up), scaled_f16x2(u.y, up), scaled_f16x2(u.z, up), scaled_f16x2(u.w, up));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int wr = quarter * 32 + h0 + i * RPI + lane / LPR, ci = lane % LPR;
+                        float mx = fmaxf(fmaxf(amax_bf16x2(u[i].x), amax_bf16x2(u[i].y)), fmaxf(amax_bf16x2(u[i].z), amax_bf16x2(u[i].w)));
+#pragma unroll
+                        for (int k2 = LPR / 2; k2; k2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k2));
+                        const int e = row_exponent(mx);
+                        const float up = row_up(e, a.scale_log2);
+                        *reinterpret_cast<uint4*>(qx + (ci >> 3) * (128 * 128) + wr * 128 + (((ci & 7) ^ (wr & 7)) << 4)) =
+                            make_uint4(scaled_f16x2(u[i].x, up), scaled_f16x2(u[i].y, up), scaled_f16x2(u[i].z, up), scaled_f16x2(u[i].w, up));
+                        // the row's own thread takes its factor
+                        const float down = __shfl_sync(0xffffffffu, row_down(e, a.scale_log2), (lane % RPI) * LPR);
+                        if ((lane - h0) / RPI == i && lane >= h0) rs = down;
+                    }
                 }
                 fence_proxy_async_smem();
                 arrive(&qfull[x]);
@@ -300,35 +322,45 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                     if (!ok) break;
                     ++tiles;
                     fence_after();
-                    const int tok0 = (it.t0 + j) * kTok;
+                    const int tok0 = (first + j) * kTok;
                     const uint64_t out = *reinterpret_cast<const volatile uint64_t*>(bad + ((all_tiles + j) & 3) * 8);
                     const bool edge = out != 0 || tok0 + kTok - 1 > pw0 || (a.window > 0 && tok0 <= pw1 - a.window);
                     auto sees = [&](int i) {  // whether this row sees the tile's token i
                         const int tk = tok0 + i;
                         return tk <= p && (a.window == 0 || tk > p - a.window) && !((out >> (8 * (i >> 4))) & 1);
                     };
-                    auto load = [&](int c, float (&v)[32]) {  // 32 of the tile's scores
-                        uint32_t u[32];
-                        ld32(ts + 32 * c, u);
-                        ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
-                    };
+                    // 32 scores at a time, the next ones on their way while these are worked on.  (Loops of two such steps
+                    // and not of all four: the roles' code shares the instruction cache.)
+                    uint32_t u0[32], u1[32];
                     float top = -INFINITY;
+                    if (edge) {
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float v[32], t0 = -INFINITY, t1 = -INFINITY;
-                        load(c, v);
-                        if (edge) {
+                        for (int c = 0; c < 4; ++c) {
+                            ld32(ts + 32 * c, u0);
+                            ld_wait(u0);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = sees(32 * c + i) ? v[i] : -INFINITY;
+                            for (int i = 0; i < 32; ++i) top = fmaxf(top, sees(32 * c + i) ? __uint_as_float(u0[i]) : -INFINITY);
                         }
+                    } else {
+                        ld32(ts, u0);
+                        float t0 = -INFINITY, t1 = -INFINITY;
+                        auto most = [&](const uint32_t* u) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            t0 = fmaxf(t0, fmaxf(v[i], v[i + 1]));
-                            t1 = fmaxf(t1, fmaxf(v[i + 2], v[i + 3]));
+                            for (int i = 0; i < 32; i += 4) {
+                                t0 = fmaxf(t0, fmaxf(__uint_as_float(u[i]), __uint_as_float(u[i + 1])));
+                                t1 = fmaxf(t1, fmaxf(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3])));
+                            }
+                        };
+#pragma unroll 1
+                        for (int c = 0; c < 128; c += 64) {
+                            ld_wait(u0);
+                            ld32(ts + c + 32, u1);
+                            most(u0);
+                            ld_wait(u1);
+                            ld32(ts + ((c + 64) & 127), u0);  // at the end the first ones again, for the exponentials
+                            most(u1);
                         }
-                        top = fmaxf(top, fmaxf(t0, t1));
+                        top = fmaxf(t0, t1);
                     }
                     top = top == -INFINITY ? top : __fmul_rn(top, rs);
                     if (__any_sync(0xffffffffu, top > m + 8.f)) {
@@ -341,7 +373,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                             for (int c = 0; c < D; c += 32) {
                                 uint32_t u[32];
                                 ld32(to + c, u);
-                                ld_wait();
+                                ld_wait(u);
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
                                 st32(to + c, u);
@@ -355,14 +387,16 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                         // The careful form rounds twice, as the reference does: the largest score's exponent is 0 whatever
                         // its size.  One rounding (below) leaves up to half an ulp of the reference there, less than 1
                         // below 2^24, the same for the whole row.
+                        if (!edge) ld_wait(u0);
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
-                            float v[32];
-                            load(c, v);
                             uint32_t pk[16];
+                            ld32(ts + 32 * c, u0);
+                            ld_wait(u0);
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) {
-                                float2 e2 = make_float2(ex2(__fsub_rn(__fmul_rn(v[i], rs), ref)), ex2(__fsub_rn(__fmul_rn(v[i + 1], rs), ref)));
+                                float2 e2 = make_float2(ex2(__fsub_rn(__fmul_rn(__uint_as_float(u0[i]), rs), ref)),
+                                                        ex2(__fsub_rn(__fmul_rn(__uint_as_float(u0[i + 1]), rs), ref)));
                                 e2.x = sees(32 * c + i) ? e2.x : 0.f;
                                 e2.y = sees(32 * c + i + 1) ? e2.y : 0.f;
                                 sum = __fadd2_rn(sum, e2);
@@ -372,19 +406,26 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                         }
                     } else {
                         const float2 rs2 = make_float2(rs, rs), ref2 = make_float2(-ref, -ref);
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            float v[32];
-                            load(c, v);
-                            uint32_t pk[16];
+                        auto exponentials = [&](const uint32_t* u, uint32_t* pk) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) {
-                                const float2 y = __ffma2_rn(make_float2(v[i], v[i + 1]), rs2, ref2);
+                                const float2 y = __ffma2_rn(make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), rs2, ref2);
                                 const float2 e2 = make_float2(ex2(y.x), ex2(y.y));
                                 sum = __fadd2_rn(sum, e2);
                                 pk[i / 2] = pack_f16x2(e2.x, e2.y);
                             }
-                            st16(ts + 16 * c, pk);
+                        };
+#pragma unroll 1
+                        for (int c = 0; c < 128; c += 64) {
+                            uint32_t pk[16];
+                            ld_wait(u0);
+                            ld32(ts + c + 32, u1);
+                            exponentials(u0, pk);
+                            st16(ts + c / 2, pk);
+                            ld_wait(u1);
+                            if (c == 0) ld32(ts + 64, u0);
+                            exponentials(u1, pk);
+                            st16(ts + c / 2 + 16, pk);
                         }
                     }
                     l += sum.x + sum.y;
@@ -398,17 +439,19 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             }
             all_tiles += cnt;
             // O: to its rows, or as this part's sums
+            const bool valid = srow < it.rows;
+            const int r = it.base + srow;
             const int64_t slot = it.parts > 1 ? (int64_t)(it.tail * it.parts + it.part) : 0;
             float* part = a.parts + slot * kRows * (D + 2);  // [D / 4][256 rows] of four values, then [256] {m, l}
             const float inv = l > 0.f ? a.cache.v_scale / l : 0.f;
-            __nv_bfloat16* dst = a.out + qrow * a.ldo + (int64_t)head * D;
+            __nv_bfloat16* dst = a.out + (it.row0 + r / a.G) * a.ldo + (int64_t)(it.h * a.G + r % a.G) * D;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float v[32];
                 uint32_t raw[32];
                 if (active && ok) {
                     ld32(to + c, raw);
-                    ld_wait();
+                    ld_wait(raw);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) raw[i] = 0u;
@@ -484,109 +527,121 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             }
         }
     } else if (warp < kMmaWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDqRegs));
-        const bool isv = warp >= kSoftWarps + kDqWarps;
-        const int id = threadIdx.x - (isv ? kSoftWarps + kDqWarps : kSoftWarps) * 32;  // 0 .. 127
+        const int id = threadIdx.x - kSoftWarps * 32;  // 0 .. 127
         // K: token id of the tile.  V: 16 values, block id / 16, of 8 tokens from 8 (id % 16)
-        const int vblk = id >> 4, vch = id & 15, at = isv ? vch * 8 : id;
-        const bool use = !isv || vblk < D / 16;
-        constexpr int CW = 16;                 // words of codes a thread at most
+        const int vblk = id >> 4, vch = id & 15;
+        const bool vuse = vblk < D / 16;
         constexpr int KW = D / 8, KS = D / 64;  // words of codes and of scales of a token's K
         int k = 0;
-        auto next_item = [&](Item& to) {  // the next one that has tokens
+        auto next_item = [&]() {  // the next one that has tokens
             while (k < rounds) {
-                to = item(k++);
+                const Item& to = take(k++);
                 if (to.b >= 0 && to.t1 > to.t0) return true;
             }
             return false;
         };
-        // a tile that this thread has looked up: the group of its token, or NULL (behind the end, a bad page)
+        // a tile that this thread has looked up: the groups of its tokens, or NULL (behind the end, a bad page)
         struct Place {
-            const uint8_t* g;
-            int left;  // tokens from this thread's to the context's end
-            bool bad;
+            const uint8_t *k, *v;
+            int left;  // tokens from V's first one to the context's end
+            bool bad, some;
         };
-        Item it = {};
-        int tile = 0;
-        bool more = true;
-        auto step = [&]() {  // on to the next tile, its page looked up
-            Place pl = {nullptr, 0, false};
-            if (more && ++tile >= it.t1) {
-                more = next_item(it);
-                tile = it.t0;
-            }
-            if (!more || !use) return pl;
-            const int tok = tile * kTok + at;
-            pl.left = it.L - tok;
-            if (pl.left <= 0) return pl;
+        const Item& it = slots[warp];
+        bool more = next_item();
+        int tile = more ? it.t0 - 1 : 0;
+        auto group = [&](int tok, bool& bad_page) -> const uint8_t* {
+            if (tok >= it.L) return nullptr;
             const int page = __ldg(a.table + it.b * a.ldb + (tok >> a.cache.page_log));
             if (page < 0 || page >= a.cache.n_pages) {
                 atomicOr(a.status, kStatusBad);
-                pl.bad = true;
-                return pl;
+                bad_page = true;
+                return nullptr;
             }
-            pl.g = group_ptr<D>(a.cache, page, it.h, tok & ((1 << a.cache.page_log) - 1));
+            return group_ptr<D>(a.cache, page, it.h, tok & ((1 << a.cache.page_log) - 1));
+        };
+        auto step = [&]() {  // on to the next tile
+            Place pl = {nullptr, nullptr, 0, false, false};
+            if (more && ++tile >= it.t1) {
+                more = next_item();
+                tile = it.t0;
+            }
+            if (!more) return pl;
+            bool ignored = false;
+            pl.some = true;
+            pl.k = group(tile * kTok + id, pl.bad);
+            pl.v = vuse ? group(tile * kTok + vch * 8, ignored) : nullptr;
+            pl.left = it.L - (tile * kTok + vch * 8);
             return pl;
         };
-        uint64_t *full = isv ? vfull : kfull, *free_ = isv ? vfree : kfree;
-        auto fetch = [&](const Place& pl, uint32_t (&c)[CW], uint32_t (&sc)[2]) {
-#pragma unroll
-            for (int i = 0; i < CW; ++i) c[i] = 0u;
-            sc[0] = sc[1] = 0u;
-            if (!pl.g) return;
-            const int r = at & 15;  // V: 0 or 8
-            const uint4* src = reinterpret_cast<const uint4*>(isv ? pl.g + v_code_off(D) + vblk * 128 + r * 8 : pl.g + r * (D / 2));
-            const uint32_t* ssrc =
-                reinterpret_cast<const uint32_t*>(isv ? pl.g + v_scale_off(D) + vblk * 16 + r : pl.g + k_scale_off(D) + r * (D / 16));
-#pragma unroll
-            for (int i = 0; i < CW / 4; ++i) {
-                if (i >= KW / 4 && !isv) break;
-                const uint4 u = __ldg(src + i);
-                c[4 * i] = u.x, c[4 * i + 1] = u.y, c[4 * i + 2] = u.z, c[4 * i + 3] = u.w;
-            }
-            sc[0] = __ldg(ssrc);
-            if (isv || KS > 1) sc[1] = __ldg(ssrc + 1);
+        struct Codes {
+            uint32_t k[KW], ks[KS], v[16], vs[2];
         };
-        uint32_t c[CW], sc[2];
-        Place now, next;
-        bool cur = next_item(it);  // whether `now` is a tile
-        more = cur;
-        tile = it.t0 - 1;
-        now = step();
-        fetch(now, c, sc);
-        bool nmore = cur;
-        next = step();
-        nmore = more;
-        for (int tiles = 0; cur; ++tiles) {
+        auto fetch = [&](const Place& pl, Codes& c) {
+#pragma unroll
+            for (int i = 0; i < KW; ++i) c.k[i] = 0u;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) c.ks[i] = 0u;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) c.v[i] = 0u;
+            c.vs[0] = c.vs[1] = 0u;
+            if (pl.k) {
+                const int r = id & 15;
+#pragma unroll
+                for (int i = 0; i < KW / 4; ++i) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(pl.k + r * (D / 2)) + i);
+                    c.k[4 * i] = u.x, c.k[4 * i + 1] = u.y, c.k[4 * i + 2] = u.z, c.k[4 * i + 3] = u.w;
+                }
+#pragma unroll
+                for (int i = 0; i < KS; ++i) c.ks[i] = __ldg(reinterpret_cast<const uint32_t*>(pl.k + k_scale_off(D) + r * (D / 16)) + i);
+            }
+            if (pl.v) {
+                const int r = (vch * 8) & 15;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(pl.v + v_code_off(D) + vblk * 128 + r * 8) + i);
+                    c.v[4 * i] = u.x, c.v[4 * i + 1] = u.y, c.v[4 * i + 2] = u.z, c.v[4 * i + 3] = u.w;
+                }
+                const uint2 u = __ldg(reinterpret_cast<const uint2*>(pl.v + v_scale_off(D) + vblk * 16 + r));
+                // places behind the end hold anything: scale 0, so that 0 * value is 0
+                const int left = pl.left;
+                c.vs[0] = left >= 4 ? u.x : u.x & ((1u << (8 * left)) - 1u);
+                c.vs[1] = left >= 8 ? u.y : left <= 4 ? 0u : u.y & ((1u << (8 * (left - 4))) - 1u);
+            }
+        };
+        Codes c;
+        Place now = step();
+        fetch(now, c);
+        Place next = step();
+        for (int tiles = 0; now.some; ++tiles) {
             const int s = tiles & 1;
-            uint32_t nc[CW], nsc[2];
-            fetch(next, nc, nsc);
+            Codes nc;
+            fetch(next, nc);
             const Place ahead = step();
-            const bool amore = more;
-            if (tiles >= 2 && !wait(&free_[s], ((tiles >> 1) - 1) & 1)) break;
-            if (!isv) {
+            if (tiles >= 2 && !wait(&kfree[s], ((tiles >> 1) - 1) & 1)) break;
+            {
                 uint8_t* dst = kt + s * C::kKBytes + id * 128;
 #pragma unroll
                 for (int w = 0; w < KW; w += 2) {  // 16 values under one scale
-                    const uint32_t two = e4m3x2_to_f16x2((sc[w / 8] >> (8 * ((w / 2) & 3))) & 0xffu);
+                    const uint32_t two = e4m3x2_to_f16x2((c.ks[w / 8] >> (8 * ((w / 2) & 3))) & 0xffu);
                     const uint32_t f = __byte_perm(two, 0, 0x1010);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         uint32_t h[4];
-                        e2m1x8(c[w + u], h);
+                        e2m1x8(c.k[w + u], h);
                         const int piece = w + u;  // 8 values: 16 bytes
                         *reinterpret_cast<uint4*>(dst + (piece >> 3) * (kTok * 128) + (((piece & 7) ^ (id & 7)) << 4)) =
                             make_uint4(hmul2(h[0], f), hmul2(h[1], f), hmul2(h[2], f), hmul2(h[3], f));
                     }
                 }
                 if ((id & 15) == 0) bad[(tiles & 3) * 8 + (id >> 4)] = now.bad ? 1 : 0;
-            } else if (use) {
+            }
+            fence_proxy_async_smem();
+            arrive(&kfull[s]);
+            if (tiles >= 2 && !wait(&vfree[s], ((tiles >> 1) - 1) & 1)) break;
+            if (vuse) {
                 uint8_t* dst = vt + s * C::kVBytes + (vch >> 3) * (D * 128);
-                // places behind the end hold anything: scale 0, so that 0 * value is 0
-                const uint32_t s0 = now.left >= 4 ? sc[0] : now.left <= 0 ? 0u : sc[0] & ((1u << (8 * now.left)) - 1u);
-                const uint32_t s1 = now.left >= 8 ? sc[1] : now.left <= 4 ? 0u : sc[1] & ((1u << (8 * (now.left - 4))) - 1u);
-                const uint32_t f[4] = {e4m3x2_to_f16x2(s0 & 0xffffu), e4m3x2_to_f16x2(s0 >> 16), e4m3x2_to_f16x2(s1 & 0xffffu),
-                                       e4m3x2_to_f16x2(s1 >> 16)};
+                const uint32_t f[4] = {e4m3x2_to_f16x2(c.vs[0] & 0xffffu), e4m3x2_to_f16x2(c.vs[0] >> 16),
+                                       e4m3x2_to_f16x2(c.vs[1] & 0xffffu), e4m3x2_to_f16x2(c.vs[1] >> 16)};
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {  // a word of each token: 8 of the 16 values
                     constexpr uint32_t lo = 0x0f0f0f0fu;
@@ -595,7 +650,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                         uint32_t x[4][4];                // [token pair][byte]
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint32_t p0 = c[4 * i + w], p1 = c[4 * i + 2 + w];
+                            const uint32_t p0 = c.v[4 * i + w], p1 = c.v[4 * i + 2 + w];
                             e2m1x8(odd ? ((p0 >> 4) & lo) | (p1 & ~lo) : (p0 & lo) | ((p1 << 4) & ~lo), x[i]);
                         }
 #pragma unroll
@@ -608,12 +663,9 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                 }
             }
             fence_proxy_async_smem();
-            arrive(&full[s]);
-#pragma unroll
-            for (int i = 0; i < CW; ++i) c[i] = nc[i];
-            sc[0] = nsc[0], sc[1] = nsc[1];
+            arrive(&vfull[s]);
+            c = nc;
             now = next, next = ahead;
-            cur = nmore, nmore = amore;
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
@@ -632,7 +684,8 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             commit(&sfull[x]);
         };
         for (int k = 0; k < rounds && ok; ++k) {
-            const Item it = item(k);
+            slots[warp] = item(k);
+            const Item& it = slots[warp];
             if (it.b < 0 || it.t1 <= it.t0) continue;
             const int cnt = it.t1 - it.t0, two = it.rows > 128 ? 2 : 1;
             for (int x = 0; x < two && ok; ++x) {
