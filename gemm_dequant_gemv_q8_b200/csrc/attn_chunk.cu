@@ -44,28 +44,33 @@ struct Cfg {
 };
 static_assert(Cfg<128>::smem(kMaxSeqs) <= 232448, "shared memory");
 
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr) {  // K-major, 128-byte swizzle
-    uint64_t d = (uint64_t)((saddr >> 4) & 0x3fffu);
-    d |= (uint64_t)1 << 16;            // leading byte offset (unused for swizzled K-major)
-    d |= (uint64_t)(1024 >> 4) << 32;  // stride byte offset: 8-row groups 1024 B apart
-    d |= (uint64_t)1 << 46;            // descriptor version for sm_100
-    d |= (uint64_t)2 << 61;            // 128-byte swizzle
-    return d;
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The low word of a shared-memory descriptor (address, unused leading offset); the high word is the same for every
+// operand here: 8-row groups 1024 bytes apart, the sm_100 version, 128-byte swizzle (K-major).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr >> 4) & 0x3fffu) | (1u << 16); }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+// One thread of the converged warp issues; the operands are the same in all of it, so they stay in uniform registers.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n .reg .pred p, e;\n .reg .b64 da, db;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+        " setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate),
+        "n"(kDescHi)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n .reg .pred p, e;\n .reg .b64 db;\n mov.b64 db, {%2, %5};\n"
+        " setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate),
+        "n"(kDescHi)
         : "memory");
 }
+// Commits the elected thread's products: elect.sync picks the same thread each time.
 __device__ __forceinline__ void commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+        : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -669,63 +674,65 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
-        if (warp == kMmaWarp && lane == 0) {
-        const uint32_t idesc_s = (1u << 4) | ((uint32_t)(kTok >> 3) << 17) | ((128u >> 4) << 24);  // fp16 x fp16 -> fp32
-        const uint32_t idesc_o = (1u << 4) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
-        int tiles = 0, q_its[2] = {0, 0}, p_tiles[2] = {0, 0};
-        bool ok = true;
-        const uint32_t sq = smem_u32(qt), sk = smem_u32(kt), sv = smem_u32(vt);
-        auto scores = [&](int x, int s) {
+        if (warp == kMmaWarp) {
+            const uint32_t idesc_s = (1u << 4) | ((uint32_t)(kTok >> 3) << 17) | ((128u >> 4) << 24);  // fp16 x fp16 -> fp32
+            const uint32_t idesc_o = (1u << 4) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
+            int tiles = 0, q_its[2] = {0, 0}, p_tiles[2] = {0, 0};
+            bool ok = true;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t dq = desc_lo(smem_u32(qt)), dk = desc_lo(smem_u32(kt)), dv = desc_lo(smem_u32(vt));
+            auto warp_wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+            auto scores = [&](int x, int s) {
+                const uint32_t qa = dq + x * (C::kQBytes >> 4), ka = dk + s * (C::kKBytes >> 4), d = tm + x * 128;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const uint32_t at = (i >> 2) * (128 * 128) + (i & 3) * 32;
-                mma_ss(tmem + x * 128, sdesc(sq + x * C::kQBytes + at), sdesc(sk + s * C::kKBytes + at), idesc_s, i > 0);
-            }
-            commit(&sfull[x]);
-        };
-        for (int k = 0; k < rounds && ok; ++k) {
-            slots[warp] = item(k);
-            const Item& it = slots[warp];
-            if (it.b < 0 || it.t1 <= it.t0) continue;
-            const int cnt = it.t1 - it.t0, two = it.rows > 128 ? 2 : 1;
-            for (int x = 0; x < two && ok; ++x) {
-                ok = wait(&qfull[x], q_its[x] & 1);
-                ++q_its[x];
-            }
-            ok = ok && wait(&kfull[tiles & 1], (tiles >> 1) & 1);
-            if (!ok) break;
-            fence_after();
-            for (int x = 0; x < two; ++x) scores(x, tiles & 1);
-            commit(&kfree[tiles & 1]);
-            for (int j = 0; j < cnt && ok; ++j, ++tiles) {
-                const int s = tiles & 1, sn = (tiles + 1) & 1;
-                ok = wait(&vfull[s], (tiles >> 1) & 1);
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint32_t at = ((i >> 2) * (128 * 128) + (i & 3) * 32) >> 4;
+                    mma_ss(d, qa + at, ka + at, idesc_s, i > 0);
+                }
+                commit(&sfull[x]);
+            };
+            for (int k = 0; k < rounds && ok; ++k) {
+                const Item& it = take(k);
+                if (it.b < 0 || it.t1 <= it.t0) continue;
+                const int cnt = it.t1 - it.t0, two = it.rows > 128 ? 2 : 1;
                 for (int x = 0; x < two && ok; ++x) {
-                    ok = wait(&pfull[x], p_tiles[x] & 1);
-                    ++p_tiles[x];
-                    if (!ok) break;
-                    fence_after();
+                    ok = warp_wait(&qfull[x], q_its[x] & 1);
+                    ++q_its[x];
+                }
+                ok = ok && warp_wait(&kfull[tiles & 1], (tiles >> 1) & 1);
+                if (!ok) break;
+                fence_after();
+                for (int x = 0; x < two; ++x) scores(x, tiles & 1);
+                commit(&kfree[tiles & 1]);
+                for (int j = 0; j < cnt && ok; ++j, ++tiles) {
+                    const int s = tiles & 1, sn = (tiles + 1) & 1;
+                    ok = warp_wait(&vfull[s], (tiles >> 1) & 1);
+                    for (int x = 0; x < two && ok; ++x) {
+                        ok = warp_wait(&pfull[x], p_tiles[x] & 1);
+                        ++p_tiles[x];
+                        if (!ok) break;
+                        fence_after();
+                        const uint32_t d = tm + 256 + x * D, pa = tm + x * 128, va = dv + s * (C::kVBytes >> 4);
 #pragma unroll
-                    for (int i = 0; i < kTok / 16; ++i)
-                        mma_ts(tmem + 256 + x * D, tmem + x * 128 + i * 8, sdesc(sv + s * C::kVBytes + (i >> 2) * (D * 128) + (i & 3) * 32),
-                               idesc_o, j > 0 || i > 0);
-                    if (x == two - 1) commit(&vfree[s]);
-                    if (j + 1 < cnt) {
-                        if (x == 0) {
-                            ok = wait(&kfull[sn], ((tiles + 1) >> 1) & 1);
-                            if (!ok) break;
-                            fence_after();
+                        for (int i = 0; i < kTok / 16; ++i)
+                            mma_ts(d, pa + i * 8, va + (((i >> 2) * (D * 128) + (i & 3) * 32) >> 4), idesc_o, j > 0 || i > 0);
+                        if (x == two - 1) commit(&vfree[s]);
+                        if (j + 1 < cnt) {
+                            if (x == 0) {
+                                ok = warp_wait(&kfull[sn], ((tiles + 1) >> 1) & 1);
+                                if (!ok) break;
+                                fence_after();
+                            }
+                            scores(x, sn);
+                            if (x == two - 1) commit(&kfree[sn]);
+                        } else {
+                            commit(&ofull[x]);
                         }
-                        scores(x, sn);
-                        if (x == two - 1) commit(&kfree[sn]);
-                    } else {
-                        commit(&ofull[x]);
                     }
                 }
             }
-        }
-        commit(mma_done);  // every tensor-core operation of this thread is done before the teardown
-        if (!mbar_wait_bounded(mma_done, 0)) atomicOr(a.status, 1u);
+            commit(mma_done);  // every tensor-core operation of this warp is done before the teardown
+            if (!mbar_wait_bounded(mma_done, 0)) atomicOr(a.status, 1u);
         }
     }
     fence_before();
