@@ -389,7 +389,7 @@ class KVCache:
             raise TypeError("data must be a contiguous uint8 CUDA tensor")
         if data.numel() == 0 or data.numel() % per:
             raise ValueError(f"data must hold whole pages of {per} bytes")
-        self.data, self.page, self.Hkv, self.D = data, page, Hkv, D
+        self.data, self.page, self.Hkv, self.D, self.index = data, page, Hkv, D, data.get_device()
         self.n_pages = data.numel() // per
         self.desc = KVCacheDesc(data.data_ptr(), self.n_pages, page, Hkv, D, k_scale, v_scale)
         self.ref = ctypes.addressof(self.desc)
@@ -403,80 +403,108 @@ def kv_cache(n_pages, page, Hkv, D, k_scale=1.0, v_scale=1.0, device="cuda"):
     return KVCache(_alloc_aligned(nbytes, device).zero_(), page, Hkv, D, k_scale, v_scale)
 
 
-def _ptr(t, name, dtype, device, shape=None):
-    """Address of a CUDA tensor on `device` (None for None): its dtype, last stride and shape checked."""
+# A decode step makes these calls once a layer, so what the binding itself costs counts: device numbers instead of device
+# objects, the raw stream handle, and each argument looked at once.
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _ptr(t, name, dtype, index, shape=None):
+    """Address of a contiguous CUDA tensor on device `index` (None for None), its dtype and shape checked."""
     if t is None:
         return None
-    if not t.is_cuda or t.dtype != dtype or t.device != device:
-        raise TypeError(f"{name} must be a {dtype} tensor on {device}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
+    if t.dtype is not dtype or t.get_device() != index:
+        raise TypeError(f"{name} must be a {dtype} tensor on cuda:{index}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _rows(t, name, heads, D):
-    """(T, row stride) of T rows of heads * D contiguous values: (T, heads * D) or (T, heads, D)."""
-    if t.dim() == 3:
-        if t.shape[1] != heads or t.shape[2] != D or (heads > 1 and t.stride(1) != D):
-            raise ValueError(f"{name} must be (T, {heads}, {D}) with each row's heads contiguous")
-    elif t.dim() != 2 or t.shape[1] != heads * D:
-        raise ValueError(f"{name} must be (T, {heads * D}) or (T, {heads}, {D})")
-    T = t.shape[0]
-    return T, (t.stride(0) if T > 1 else heads * D)
+def _rows(t, name, dtype, index, T, heads, D):
+    """(address, row stride) of T rows of heads * D contiguous values: (T, heads, D) or (T, heads * D)."""
+    if t.dtype is not dtype or t.get_device() != index:
+        raise TypeError(f"{name} must be a {dtype} tensor on cuda:{index}")
+    shape = t.shape
+    if shape != (T, heads, D) and shape != (T, heads * D):
+        raise ValueError(f"{name} must be ({T}, {heads}, {D}) or ({T}, {heads * D}), got {tuple(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), heads * D
+    st = t.stride()
+    if (st[-1] != 1 and D > 1) or (len(st) == 3 and heads > 1 and st[1] != D):
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return t.data_ptr(), st[0] if T > 1 else heads * D
 
 
-def _call(fn, device, stream, *args):
-    """fn(*args, stream) with `device` current (the library works on the current device)."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream must be on {device}")
-    if device.index == torch.cuda.current_device():
-        s = torch.cuda.current_stream(device) if stream is None else stream
-        st = getattr(lib(), fn)(*args, s.cuda_stream)
+def _x_rows(x, width, exact):
+    """(dtype code, device, rows, row stride) of the projections' rows."""
+    xdt = _XDT.get(x.dtype)
+    if xdt is None or not x.is_cuda or x.dim() != 2:
+        raise TypeError("x must be a 2-d float32 or bfloat16 CUDA tensor")
+    T, W = x.shape
+    if W != width and (exact or W < width):
+        raise ValueError(f"x must have {'' if exact else 'at least '}{width} columns, got {W}")
+    ld = x.stride(0)
+    if x.stride(1) != 1:
+        raise ValueError("x rows must be contiguous")
+    return xdt, x.get_device(), T, ld if T > 1 else W
+
+
+def _ws(ws, nbytes, index):
+    """(address, bytes) of a workspace, a fresh one where none is given."""
+    if ws is None:
+        ws = workspace(nbytes, torch.device("cuda", index))
+    elif ws.get_device() != index or not ws.is_contiguous():
+        raise TypeError(f"ws must be a contiguous tensor on cuda:{index}")
+    return ws, ws.data_ptr(), ws.nbytes
+
+
+def _call(fn, index, stream, *args):
+    """fn(*args, stream) with device `index` current (the library works on the current device)."""
+    if stream is not None and stream.device_index != index:
+        raise ValueError(f"the stream must be on cuda:{index}")
+    f = getattr(_lib or lib(), fn)
+    if _get_device() == index:
+        st = f(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     else:
-        with torch.cuda.device(device):
-            s = torch.cuda.current_stream(device) if stream is None else stream
-            st = getattr(lib(), fn)(*args, s.cuda_stream)
-    _check(fn, st)
+        with torch.cuda.device(index):
+            st = f(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if st != 0:
+        raise QlinError(fn, st)
 
 
-def _qk_params(cos_sin, q_weight, k_weight, eps, rot, flags, D, device):
+def _qk_params(cos_sin, q_weight, k_weight, eps, rot, flags, D, index):
+    n_pos, table = 0, None
     if cos_sin is None:
-        rot, n_pos = 0, 0
+        rot = 0
     else:
-        rot = cos_sin.shape[-1] if rot is None else rot
-        n_pos = cos_sin.shape[0]
-    if cos_sin is not None and rot and (cos_sin.dim() != 2 or not cos_sin.is_contiguous()):
-        raise ValueError("cos_sin must be a contiguous (positions, rot) tensor")
-    return QKParams(_ptr(q_weight, "q_weight", torch.float32, device, (D,)),
-                    _ptr(k_weight, "k_weight", torch.float32, device, (D,)),
-                    _ptr(cos_sin, "cos_sin", torch.float32, device, (n_pos, rot) if rot else None), n_pos, rot, flags, eps)
+        if cos_sin.dim() != 2 or (rot is not None and rot and cos_sin.shape[1] != rot):
+            raise ValueError("cos_sin must be (positions, rot)")
+        n_pos, width = cos_sin.shape
+        rot = width if rot is None else rot
+        table = _ptr(cos_sin, "cos_sin", torch.float32, index)
+    return QKParams(_ptr(q_weight, "q_weight", torch.float32, index, (D,)), _ptr(k_weight, "k_weight", torch.float32, index, (D,)),
+                    table, n_pos, rot, flags, eps)
 
 
 def qlin_qk_norm_rope(x, Hq, Hkv, D, positions=None, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, rot=None,
                       flags=QLIN_ROPE_HALVES, q=None, k=None, ydt=QLIN_BF16, ws=None, stream=None):
     """Norm (where a weight is given) and rotation of the query and key heads at the front of x's rows
     (T, >= (Hq + Hkv) * D).  Returns (q, k) as (T, heads, D); q and k may be x's own heads."""
-    xdt = _XDT.get(x.dtype)
-    if xdt is None or not x.is_cuda or x.dim() != 2 or x.shape[1] < (Hq + Hkv) * D or x.stride(1) != 1:
-        raise TypeError("x must be a float32 or bfloat16 CUDA tensor (T, >= (Hq + Hkv) * D) with contiguous rows")
-    dev, T = x.device, x.shape[0]
+    xdt, dev, T, ldx = _x_rows(x, (Hq + Hkv) * D, False)
     out = _YDT[ydt]
     if q is None:
-        q = torch.empty(T, Hq, D, dtype=out, device=dev)
+        q = torch.empty((T, Hq, D), dtype=out, device=x.device)
     if k is None:
-        k = torch.empty(T, Hkv, D, dtype=out, device=dev)
-    if ws is None:
-        ws = workspace(256, dev)
-    Tq, ldq = _rows(q, "q", Hq, D)
-    Tk, ldk = _rows(k, "k", Hkv, D)
-    if Tq != T or Tk != T:
-        raise ValueError("q and k must have x's rows")
+        k = torch.empty((T, Hkv, D), dtype=out, device=x.device)
+    pq, ldq = _rows(q, "q", out, dev, T, Hq, D)
+    pk, ldk = _rows(k, "k", out, dev, T, Hkv, D)
+    ws, pw, nw = _ws(ws, 256, dev)
     par = _qk_params(cos_sin, q_weight, k_weight, eps, rot, flags, D, dev)
-    _call("qlin_qk_norm_rope", dev, stream, x.data_ptr(), xdt, T, x.stride(0) if T > 1 else x.shape[1], Hq, Hkv, D,
-          ctypes.addressof(par), _ptr(positions, "positions", torch.int32, dev, (T,)), _ptr(q, "q", out, dev), ldq,
-          _ptr(k, "k", out, dev), ldk, ydt, 0, _ptr(ws, "ws", torch.uint8, dev), ws.numel())
+    _call("qlin_qk_norm_rope", dev, stream, x.data_ptr(), xdt, T, ldx, Hq, Hkv, D, ctypes.addressof(par),
+          _ptr(positions, "positions", torch.int32, dev, (T,)), pq, ldq, pk, ldk, ydt, 0, pw, nw)
     return q, k
 
 
@@ -485,41 +513,29 @@ def qlin_kv_append(cache, x, Hq, positions, slots, cos_sin=None, q_weight=None, 
     """Append the tokens of x's rows (T, (Hq + 2 Hkv) * D: [q | k | v], fp32 or bf16) to the cache at `slots`
     (int32; -1: a padding row).  Returns the normed and rotated queries, (T, Hq, D) bf16."""
     Hkv, D = cache.Hkv, cache.D
-    xdt = _XDT.get(x.dtype)
-    if xdt is None or not x.is_cuda or x.dim() != 2 or x.shape[1] != (Hq + 2 * Hkv) * D or x.stride(1) != 1:
-        raise TypeError("x must be a float32 or bfloat16 CUDA tensor (T, (Hq + 2 Hkv) * D) with contiguous rows")
-    dev, T = x.device, x.shape[0]
-    if cache.data.device != dev:
-        raise ValueError(f"the cache must be on {dev}")
+    xdt, dev, T, ldx = _x_rows(x, (Hq + 2 * Hkv) * D, True)
+    if cache.index != dev:
+        raise ValueError(f"the cache must be on cuda:{dev}")
     if q is None:
-        q = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
-    if ws is None:
-        ws = workspace(256, dev)
-    Tq, ldq = _rows(q, "q", Hq, D)
-    if Tq != T:
-        raise ValueError("q must have x's rows")
+        q = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=x.device)
+    pq, ldq = _rows(q, "q", torch.bfloat16, dev, T, Hq, D) if Hq else (None, 0)
+    ws, pw, nw = _ws(ws, 256, dev)
     par = _qk_params(cos_sin, q_weight, k_weight, eps, rot, flags, D, dev)
-    _call("qlin_kv_append", dev, stream, cache.ref, x.data_ptr(), xdt, T, x.stride(0) if T > 1 else x.shape[1], Hq,
-          ctypes.addressof(par), _ptr(positions, "positions", torch.int32, dev, (T,)),
-          _ptr(slots, "slots", torch.int32, dev, (T,)), _ptr(q, "q", torch.bfloat16, dev) if Hq else None, ldq, 0,
-          _ptr(ws, "ws", torch.uint8, dev), ws.numel())
+    _call("qlin_kv_append", dev, stream, cache.ref, x.data_ptr(), xdt, T, ldx, Hq, ctypes.addressof(par),
+          _ptr(positions, "positions", torch.int32, dev, (T,)), _ptr(slots, "slots", torch.int32, dev, (T,)), pq, ldq, 0, pw, nw)
     return q
 
 
 def qlin_kv_gather(cache, slots, k=None, v=None, ydt=QLIN_BF16, ws=None, stream=None):
     """The values that slots of the cache stand for: (k, v), each (T, Hkv, D) fp32 or bf16."""
-    dev, T = cache.data.device, slots.shape[0]
-    out, shape = _YDT[ydt], (slots.shape[0], cache.Hkv, cache.D)
+    dev, out, shape = cache.index, _YDT[ydt], (slots.shape[0], cache.Hkv, cache.D)
     if k is None:
-        k = torch.empty(shape, dtype=out, device=dev)
+        k = torch.empty(shape, dtype=out, device=cache.data.device)
     if v is None:
-        v = torch.empty(shape, dtype=out, device=dev)
-    if not k.is_contiguous() or not v.is_contiguous():
-        raise ValueError("k and v must be contiguous")
-    if ws is None:
-        ws = workspace(256, dev)
-    _call("qlin_kv_gather", dev, stream, cache.ref, T, _ptr(slots, "slots", torch.int32, dev, (T,)),
-          _ptr(k, "k", out, dev, shape), _ptr(v, "v", out, dev, shape), ydt, _ptr(ws, "ws", torch.uint8, dev), ws.numel())
+        v = torch.empty(shape, dtype=out, device=cache.data.device)
+    ws, pw, nw = _ws(ws, 256, dev)
+    _call("qlin_kv_gather", dev, stream, cache.ref, shape[0], _ptr(slots, "slots", torch.int32, dev, shape[:1]),
+          _ptr(k, "k", out, dev, shape), _ptr(v, "v", out, dev, shape), ydt, pw, nw)
     return k, v
 
 
@@ -531,25 +547,21 @@ def qlin_attn_kv4(cache, q, block_table, seq_lens, cu_q, max_q, scale=None, wind
     """Causal attention of B sequences' last tokens over the cache.  q: (total_q, Hq, D) bf16; block_table: (B,
     pages) int32; seq_lens: (B,) int32, each context with the call's own tokens; cu_q: (B + 1,) int32, the
     sequences' first rows of q; max_q: the most queries of one sequence.  Returns out, q's shape, bf16."""
-    if q.dim() != 3 or q.shape[2] != cache.D:
-        raise ValueError(f"q must be (total_q, Hq, {cache.D})")
-    dev, D, Hq, B = q.device, cache.D, q.shape[1], seq_lens.shape[0]
-    if cache.data.device != dev:
-        raise ValueError(f"the cache must be on {dev}")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be (B, pages)")
-    total, ldq = _rows(q, "q", Hq, D)
+    dev, D, Bf = cache.index, cache.D, torch.bfloat16
+    if q.dim() != 3:
+        raise ValueError(f"q must be (total_q, Hq, {D})")
+    total, Hq, _ = q.shape
+    pq, ldq = _rows(q, "q", Bf, dev, total, Hq, D)
     if out is None:
-        out = torch.empty(total, Hq, D, dtype=torch.bfloat16, device=dev)
-    to, ldo = _rows(out, "out", Hq, D)
-    if to != total:
-        raise ValueError("out must have q's rows")
-    if ws is None:
-        ws = workspace(qlin_attn_kv4_workspace_bytes(cache, B, max_q, Hq), dev)
+        out = torch.empty((total, Hq, D), dtype=Bf, device=q.device)
+    po, ldo = _rows(out, "out", Bf, dev, total, Hq, D)
+    B = seq_lens.shape[0]
+    if (block_table.dtype is not torch.int32 or block_table.get_device() != dev or block_table.dim() != 2
+            or block_table.shape[0] != B or block_table.stride(1) != 1):
+        raise ValueError(f"block_table must be a ({B}, pages) int32 tensor on cuda:{dev} with contiguous rows")
     pages = block_table.shape[1]
-    _call("qlin_attn_kv4", dev, stream, cache.ref, _ptr(q, "q", torch.bfloat16, dev), ldq,
-          _ptr(block_table, "block_table", torch.int32, dev), block_table.stride(0) if B > 1 else pages, pages,
-          _ptr(seq_lens, "seq_lens", torch.int32, dev), _ptr(cu_q, "cu_q", torch.int32, dev, (B + 1,)), B, max_q, total,
-          Hq, D ** -0.5 if scale is None else scale, window, _ptr(out, "out", torch.bfloat16, dev), ldo, 0,
-          _ptr(ws, "ws", torch.uint8, dev), ws.numel())
+    ws, pw, nw = _ws(ws, 0 if ws is not None else qlin_attn_kv4_workspace_bytes(cache, B, max_q, Hq), dev)
+    _call("qlin_attn_kv4", dev, stream, cache.ref, pq, ldq, block_table.data_ptr(), block_table.stride(0) if B > 1 else pages,
+          pages, _ptr(seq_lens, "seq_lens", torch.int32, dev, (B,)), _ptr(cu_q, "cu_q", torch.int32, dev, (B + 1,)), B, max_q,
+          total, Hq, D ** -0.5 if scale is None else scale, window, po, ldo, 0, pw, nw)
     return out
