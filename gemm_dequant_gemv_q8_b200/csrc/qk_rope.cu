@@ -2,9 +2,10 @@
 // NVFP4 cache, and the read-back of slots.
 //
 // Per head: n = h * w / sqrt(mean(h^2) + eps), then the first rot values in pairs (a, b) ->
-// (a c - b s, b c + a s).  A lane holds 8 values of a head (one or two 16-byte loads), D / 8 lanes a head;
-// the mean is a shuffle sum, a pair of the half-split rotation is one shuffle away.  A warp works on one
-// token and on several heads, so that the token's cosines, sines and the weights are loaded once.
+// (a c - b s, b c + a s).  Bound by memory: every value is read and written once.  A lane holds 8 values of a head
+// (one or two 16-byte loads), D / 8 lanes a head; the mean is a shuffle sum, a pair of the half-split rotation is one
+// shuffle away.  A warp works on one token and on 8 heads of one kind (queries, keys, values): their loads are all in
+// flight before the token's row of cosines and sines, which needs its position, is asked for.
 #include "kv_cache.cuh"
 
 namespace qlin {
@@ -16,7 +17,7 @@ constexpr int kRopeWarps = 4;
 struct RopeArgs {
     const void* x;
     int64_t T, ldx;
-    int Hq, Hkv, heads;  // heads: those of x that are worked on
+    int Hq, Hkv, chunks;  // chunks: warps a token
     const float *qw, *kw, *cs;
     int64_t n_pos;
     int rot;
@@ -28,20 +29,37 @@ struct RopeArgs {
     unsigned* status;
 };
 
+// 8 values as they lie in memory, and as fp32.
 template <typename X>
-__device__ __forceinline__ void load8(const X* p, float (&v)[8]) {
-    if constexpr (sizeof(X) == 4) {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw8 {
+    uint4 u[sizeof(X) / 2];
+    __device__ __forceinline__ void load(const X* p) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(w[j] << 16);
-            v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        for (int i = 0; i < (int)sizeof(X) / 2; ++i) u[i] = *(reinterpret_cast<const uint4*>(p) + i);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(X) / 2; ++i) u[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        if constexpr (sizeof(X) == 4) {
+            const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+        } else {
+            const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = __uint_as_float(w[j] << 16);
+                v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            }
         }
     }
+};
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    Raw8<float> r;
+    r.load(p);
+    r.get(v);
 }
 
 template <typename Y>
@@ -93,7 +111,7 @@ __device__ __forceinline__ void norm_rope(float (&v)[8], bool norm, const float 
         const R ms = ss * (R)(1.0 / D) + (R)eps;
         R r;
         if constexpr (sizeof(R) == 8)
-            r = 1.0 / sqrt(ms);
+            r = rsqrt(ms);
         else
             r = 1.0f / sqrtf(ms);
 #pragma unroll
@@ -134,9 +152,20 @@ __device__ __forceinline__ uint8_t quant8(const float (&v)[8], float g, uint32_t
     const float div = __fmul_rn(e4m3_to_f32(s), g);
     codes = 0u;
     if (div > 0.f) {
+        // The reciprocal and its corrections give the correctly rounded quotient where nothing over- or underflows
+        // on the way (div_by_recip): ordinary scales, quotients below 2^60.
+        const float y = __frcp_rn(div);
+        if (div >= 0x1p-96f && div <= 0x1p96f && m * y <= 0x1p60f) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            codes |= e2m1x2_rne_sat(__fdiv_rn(v[2 * j], div), __fdiv_rn(v[2 * j + 1], div)) << (8 * j);
+            for (int j = 0; j < 4; ++j) {
+                const float2 qv = div_by_recip2(make_float2(v[2 * j], v[2 * j + 1]), div, y);
+                codes |= e2m1x2_rne_sat(qv.x, qv.y) << (8 * j);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                codes |= e2m1x2_rne_sat(__fdiv_rn(v[2 * j], div), __fdiv_rn(v[2 * j + 1], div)) << (8 * j);
+        }
     }
     return s;
 }
@@ -144,71 +173,71 @@ __device__ __forceinline__ uint8_t quant8(const float (&v)[8], float g, uint32_t
 // APPEND: heads are [q | k | v]; q to bf16 rows, k and v to the cache.  Otherwise [q | k] to rows of Y.
 template <typename X, typename Y, int D, bool INTER, bool APPEND>
 __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs a) {
-    constexpr int LPH = D / 8, HPW = 32 / LPH;  // lanes a head, heads a warp at once
+    constexpr int LPH = D / 8, HPW = 32 / LPH;         // lanes a head, heads a warp at once
+    constexpr int N = kHeadsPerWarp / HPW;             // heads a lane
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int chunks = (a.heads + kHeadsPerWarp - 1) / kHeadsPerWarp;
     const int64_t item = (int64_t)blockIdx.x * kRopeWarps + warp;
-    const int64_t t = item / chunks;
+    const int64_t t = item / a.chunks;
     if (t >= a.T) return;
-    const int h0 = (int)(item - t * chunks) * kHeadsPerWarp;
+    // this warp's heads: chunks of queries, then of keys, then of values
+    int c = (int)(item - t * a.chunks);
+    const int cq = APPEND && !a.q ? 0 : (a.Hq + kHeadsPerWarp - 1) / kHeadsPerWarp, ck = (a.Hkv + kHeadsPerWarp - 1) / kHeadsPerWarp;
+    const int kind = c < cq ? 0 : c < cq + ck ? 1 : 2;
+    c -= kind == 0 ? 0 : kind == 1 ? cq : cq + ck;
+    const int heads = kind == 0 ? a.Hq : a.Hkv, base = kind == 0 ? 0 : kind == 1 ? a.Hq : a.Hq + a.Hkv;
     const int sub = lane / LPH, d0 = (lane % LPH) * 8;
-    int slot = 0;
-    if constexpr (APPEND) {
-        slot = a.slots[t];
-        if (slot == -1) return;
+    const int h0 = c * kHeadsPerWarp + sub;            // heads h0, h0 + HPW, ..
+    const X* row = reinterpret_cast<const X*>(a.x) + t * a.ldx + (int64_t)base * D + d0;
+    Raw8<X> raw[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (h0 + i * HPW < heads)
+            raw[i].load(row + (int64_t)(h0 + i * HPW) * D);
+        else
+            raw[i].zero();
     }
+    int slot = 0;
+    if constexpr (APPEND) slot = a.slots[t];
     const int64_t pos = a.rot > 0 ? a.pos[t] : 0;
+    const float* wp = kind == 0 ? a.qw : a.kw;
+    const bool norm = kind < 2 && wp != nullptr;
+    float cs[8], sn[8], w[8];
+    if (norm) load8(wp + d0, w);
     bool bad = a.rot > 0 && (pos < 0 || pos >= a.n_pos);
-    if constexpr (APPEND) bad |= slot < 0 || ((int64_t)slot >> a.cache.page_log) >= a.cache.n_pages;
+    if constexpr (APPEND) {
+        if (slot == -1) return;
+        bad |= slot < 0 || ((int64_t)slot >> a.cache.page_log) >= a.cache.n_pages;
+    }
     if (bad) {
         if (lane == 0) atomicOr(a.status, kStatusBad);
         return;
     }
-    float c[8], s[8], qw[8], kw[8];
-    if (d0 < a.rot) load_turn<INTER>(a.cs + pos * a.rot, a.rot, d0, c, s);
-    if (a.qw) load8(a.qw + d0, qw);
-    if (a.kw) load8(a.kw + d0, kw);
-    const X* row = reinterpret_cast<const X*>(a.x) + t * a.ldx + d0;
-#pragma unroll 4
-    for (int i = 0; i < kHeadsPerWarp; i += HPW) {
-        const int h = h0 + i + sub;
-        const bool in = h < a.heads;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (in) load8(row + (int64_t)h * D, v);
-        const bool isq = h < a.Hq, isv = h >= a.Hq + a.Hkv;
-        if (__any_sync(0xffffffffu, in && isq)) {
-            float u[8];
+    if (kind < 2 && d0 < a.rot) load_turn<INTER>(a.cs + pos * a.rot, a.rot, d0, cs, sn);
+    if (!APPEND || kind == 0) {
+        Y* out = kind == 0 ? reinterpret_cast<Y*>(a.q) + t * a.ldq : reinterpret_cast<Y*>(a.k) + t * a.ldk;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) u[j] = v[j];
-            norm_rope<float, D, INTER>(u, a.qw != nullptr, qw, a.eps, a.rot, d0, c, s);
-            if (in && isq && a.q) store8(reinterpret_cast<Y*>(a.q) + t * a.ldq + (int64_t)h * D + d0, u);
+        for (int i = 0; i < N; ++i) {
+            float v[8];
+            raw[i].get(v);
+            norm_rope<float, D, INTER>(v, norm, w, a.eps, a.rot, d0, cs, sn);
+            if (h0 + i * HPW < heads) store8(out + (int64_t)(h0 + i * HPW) * D + d0, v);
         }
-        if (__any_sync(0xffffffffu, in && !isq)) {
-            if constexpr (!APPEND) {
-                norm_rope<float, D, INTER>(v, a.kw != nullptr, kw, a.eps, a.rot, d0, c, s);
-                if (in && !isq) store8(reinterpret_cast<Y*>(a.k) + t * a.ldk + (int64_t)(h - a.Hq) * D + d0, v);
-            } else {
-                if (__any_sync(0xffffffffu, in && !isq && !isv)) {
-                    float u[8];
+    } else {
+        const bool isv = kind == 2;
+        const int off = slot & ((1 << a.cache.page_log) - 1), r = off & 15;
+        const int code_at = isv ? v_code_off(D) + (d0 >> 4) * 128 + r * 8 + (d0 & 15) / 2 : r * (D / 2) + d0 / 2;
+        const int scale_at = isv ? v_scale_off(D) + (d0 >> 4) * 16 + r : k_scale_off(D) + r * (D / 16) + (d0 >> 4);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) u[j] = v[j];
-                    norm_rope<double, D, INTER>(u, a.kw != nullptr, kw, a.eps, a.rot, d0, c, s);
-                    if (!isv) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] = u[j];
-                    }
-                }
-                uint32_t codes;
-                const uint8_t sc = quant8(v, isv ? a.cache.v_scale : a.cache.k_scale, codes);
-                if (in && !isq) {
-                    const int kvh = h - a.Hq - (isv ? a.Hkv : 0);
-                    const int off = slot & ((1 << a.cache.page_log) - 1), r = off & 15;
-                    uint8_t* g = group_ptr<D>(a.cache, slot >> a.cache.page_log, kvh, off);
-                    const int code_at = isv ? v_code_off(D) + (d0 >> 4) * 128 + r * 8 + (d0 & 15) / 2 : r * (D / 2) + d0 / 2;
-                    *reinterpret_cast<uint32_t*>(g + code_at) = codes;
-                    if ((lane & 1) == 0)
-                        g[isv ? v_scale_off(D) + (d0 >> 4) * 16 + r : k_scale_off(D) + r * (D / 16) + (d0 >> 4)] = sc;
-                }
+        for (int i = 0; i < N; ++i) {
+            float v[8];
+            raw[i].get(v);
+            if (!isv) norm_rope<double, D, INTER>(v, norm, w, a.eps, a.rot, d0, cs, sn);
+            uint32_t codes;
+            const uint8_t sc = quant8(v, isv ? a.cache.v_scale : a.cache.k_scale, codes);
+            if (h0 + i * HPW < heads) {
+                uint8_t* g = group_ptr<D>(a.cache, slot >> a.cache.page_log, h0 + i * HPW, off);
+                *reinterpret_cast<uint32_t*>(g + code_at) = codes;
+                if ((lane & 1) == 0) g[scale_at] = sc;
             }
         }
     }
@@ -256,8 +285,7 @@ using namespace qlin;
 
 template <typename X, typename Y, bool APPEND>
 static cudaError_t launch_rope(const kv::RopeArgs& a, int D, bool inter, cudaStream_t s) {
-    const int64_t chunks = (a.heads + kv::kHeadsPerWarp - 1) / kv::kHeadsPerWarp;
-    const int64_t blocks = (a.T * chunks + kv::kRopeWarps - 1) / kv::kRopeWarps;
+    const int64_t blocks = (a.T * a.chunks + kv::kRopeWarps - 1) / kv::kRopeWarps;
     const dim3 grid((unsigned)blocks), block(kv::kRopeWarps * 32);
     if (D == 128)
         inter ? kv::qk_rope_kernel<X, Y, 128, true, APPEND><<<grid, block, 0, s>>>(a)
@@ -274,7 +302,9 @@ extern "C" cudaError_t qlin_launch_qk_rope(const qlin_kv_cache* cache, const voi
                                            const int32_t* slots, void* q, int64_t ldq, void* k, int64_t ldk, int ydt,
                                            void* ws, cudaStream_t s) {
     kv::RopeArgs a = {};
-    a.x = x, a.T = T, a.ldx = ldx, a.Hq = Hq, a.Hkv = Hkv, a.heads = Hq + (cache ? 2 : 1) * Hkv;
+    a.x = x, a.T = T, a.ldx = ldx, a.Hq = Hq, a.Hkv = Hkv;
+    const auto chunks = [](int heads) { return (heads + kv::kHeadsPerWarp - 1) / kv::kHeadsPerWarp; };
+    a.chunks = (cache && !q ? 0 : chunks(Hq)) + (cache ? 2 : 1) * chunks(Hkv);
     a.qw = p->q_weight, a.kw = p->k_weight, a.cs = p->cos_sin, a.n_pos = p->n_pos, a.rot = p->rot, a.eps = p->eps;
     a.pos = positions, a.slots = slots, a.q = q, a.ldq = ldq, a.k = k, a.ldk = ldk;
     a.status = (unsigned*)ws;
