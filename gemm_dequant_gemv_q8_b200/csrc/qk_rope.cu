@@ -2,10 +2,11 @@
 // NVFP4 cache, and the read-back of slots.
 //
 // Per head: n = h * w / sqrt(mean(h^2) + eps), then the first rot values in pairs (a, b) ->
-// (a c - b s, b c + a s).  Bound by memory: every value is read and written once.  A lane holds 8 values of a head
-// (one or two 16-byte loads), D / 8 lanes a head; the mean is a shuffle sum, a pair of the half-split rotation is one
-// shuffle away.  A warp works on one token and on 8 heads of one kind (queries, keys, values): their loads are all in
-// flight before the token's row of cosines and sines, which needs its position, is asked for.
+// (a c - b s, b c + a s).  Bound by memory: every value is read and written once.  A lane holds two runs of 4 values of a
+// head, D / 8 lanes a head: in the half-split rotation values i .. i + 3 and i + rot / 2 .., so that it has both members
+// of its pairs and needs no other lane; elsewhere 8 neighbours.  A warp works on one token and on 8 heads of one kind
+// (queries, keys, values): their loads are all in flight before the token's row of cosines and sines, which needs its
+// position, is asked for.
 #include "kv_cache.cuh"
 
 namespace qlin {
@@ -29,76 +30,69 @@ struct RopeArgs {
     unsigned* status;
 };
 
-// 8 values as they lie in memory, and as fp32.
+// A lane's two runs of 4 values as they lie in memory, and as fp32.
 template <typename X>
 struct Raw8 {
-    uint4 u[sizeof(X) / 2];
-    __device__ __forceinline__ void load(const X* p) {
+    uint32_t u[2][sizeof(X)];
+    __device__ __forceinline__ void load(const X* p, int d0, int d1) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(X) / 2; ++i) u[i] = *(reinterpret_cast<const uint4*>(p) + i);
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(X) / 2; ++i) u[i] = make_uint4(0, 0, 0, 0);
-    }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        if constexpr (sizeof(X) == 4) {
-            const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
-        } else {
-            const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[2 * j] = __uint_as_float(w[j] << 16);
-                v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        for (int i = 0; i < 2; ++i) {
+            const X* src = p + (i ? d1 : d0);
+            if constexpr (sizeof(X) == 4) {
+                const uint4 v = *reinterpret_cast<const uint4*>(src);
+                u[i][0] = v.x, u[i][1] = v.y, u[i][2] = v.z, u[i][3] = v.w;
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(src);
+                u[i][0] = v.x, u[i][1] = v.y;
             }
         }
     }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(X); ++i) u[0][i] = u[1][i] = 0u;
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(X) == 4)
+                    v[4 * i + j] = __uint_as_float(u[i][j]);
+                else
+                    v[4 * i + j] = __uint_as_float(j & 1 ? u[i][j / 2] & 0xffff0000u : u[i][j / 2] << 16);
+            }
+    }
 };
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    Raw8<float> r;
-    r.load(p);
-    r.get(v);
-}
 
 template <typename Y>
-__device__ __forceinline__ void store8(Y* p, const float (&v)[8]) {
+__device__ __forceinline__ void store4(Y* p, const float* v) {
     if constexpr (sizeof(Y) == 4) {
         *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        *(reinterpret_cast<float4*>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
     } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-            w[j] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+        *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     }
 }
+template <typename Y>
+__device__ __forceinline__ void store8(Y* p, const float (&v)[8]) {
+    store4(p, v);
+    store4(p + 4, v + 4);
+}
 
-// The cosines and sines of this lane's 8 values.  HALVES: of pairs i .. i + 7 with i = value % (rot / 2);
-// INTERLEAVED: of pairs value / 2 .. + 3.
+// The cosines and sines of a lane's four pairs.
 template <bool INTER>
-__device__ __forceinline__ void load_turn(const float* row, int rot, int d0, float (&c)[8], float (&s)[8]) {
-    if constexpr (INTER) {
-        const float4 a = *reinterpret_cast<const float4*>(row + d0 / 2);
-        const float4 b = *reinterpret_cast<const float4*>(row + rot / 2 + d0 / 2);
-        c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
-        s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
-    } else {
-        const int i = d0 < rot / 2 ? d0 : d0 - rot / 2;
-        load8(row + i, c);
-        load8(row + rot / 2 + i, s);
-    }
+__device__ __forceinline__ void load_turn(const float* row, int rot, int d0, float (&c)[4], float (&s)[4]) {
+    const int i = INTER ? d0 / 2 : d0;
+    const float4 a = *reinterpret_cast<const float4*>(row + i), b = *reinterpret_cast<const float4*>(row + rot / 2 + i);
+    c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
+    s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
 }
 
-// Norm (where w is given) and rotation of one head in the arithmetic of R (float, or double for keys
-// that are quantized).  Every lane of the D / 8 lanes of a head calls it; `w` and `turn` are uniform.
+// Norm (where `norm` says so) and rotation (of the lanes that `turn`) of one head in the arithmetic of R: float, or
+// double for keys that are quantized.  Every lane of the D / 8 lanes of a head calls it.
 template <typename R, int D, bool INTER>
-__device__ __forceinline__ void norm_rope(float (&v)[8], bool norm, const float (&w)[8], float eps, int rot, int d0,
-                                          const float (&c)[8], const float (&s)[8]) {
+__device__ __forceinline__ void norm_rope(float (&v)[8], bool norm, const float (&w)[8], float eps, bool turn,
+                                          const float (&c)[4], const float (&s)[4]) {
     R n[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) n[j] = (R)v[j];
@@ -113,41 +107,25 @@ __device__ __forceinline__ void norm_rope(float (&v)[8], bool norm, const float 
         if constexpr (sizeof(R) == 8)
             r = rsqrt(ms);
         else
-            r = 1.0f / sqrtf(ms);
+            r = rsqrtf(ms);  // within 2 ulp
 #pragma unroll
         for (int j = 0; j < 8; ++j) n[j] = n[j] * r * (R)w[j];
     }
-    if (rot > 0) {
-        if constexpr (INTER) {
-            if (d0 < rot) {
+    if (turn) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const R a = n[2 * j], b = n[2 * j + 1];
-                    n[2 * j] = a * (R)c[j] - b * (R)s[j];
-                    n[2 * j + 1] = b * (R)c[j] + a * (R)s[j];
-                }
-            }
-        } else {
-            const int lane = threadIdx.x & 31;
-            const bool lo = d0 < rot / 2;
-            const int other = d0 < rot ? (lo ? lane + rot / 16 : lane - rot / 16) : lane;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const R o = __shfl_sync(0xffffffffu, n[j], other);
-                if (d0 < rot) n[j] = lo ? n[j] * (R)c[j] - o * (R)s[j] : n[j] * (R)c[j] + o * (R)s[j];
-            }
+        for (int j = 0; j < 4; ++j) {
+            R &a = n[INTER ? 2 * j : j], &b = n[INTER ? 2 * j + 1 : j + 4];
+            const R x = a, y = b;
+            a = x * (R)c[j] - y * (R)s[j];
+            b = y * (R)c[j] + x * (R)s[j];
         }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = (float)n[j];
 }
 
-// Quantize this lane's 8 values (its neighbour lane ^ 1 holds the block's other 8) under scale g.
-__device__ __forceinline__ uint8_t quant8(const float (&v)[8], float g, uint32_t& codes) {
-    float m = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+// E2M1 codes of 4 values (2 bytes) of a block whose largest magnitude is m, and the block's scale byte, under scale g.
+__device__ __forceinline__ uint8_t quant4(const float* v, float m, float g, uint32_t& codes) {
     const uint8_t s = e4m3_rne_sat(__fdiv_rn(m, __fmul_rn(6.0f, g)));
     const float div = __fmul_rn(e4m3_to_f32(s), g);
     codes = 0u;
@@ -157,17 +135,20 @@ __device__ __forceinline__ uint8_t quant8(const float (&v)[8], float g, uint32_t
         const float y = __frcp_rn(div);
         if (div >= 0x1p-96f && div <= 0x1p96f && m * y <= 0x1p60f) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 const float2 qv = div_by_recip2(make_float2(v[2 * j], v[2 * j + 1]), div, y);
                 codes |= e2m1x2_rne_sat(qv.x, qv.y) << (8 * j);
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 2; ++j)
                 codes |= e2m1x2_rne_sat(__fdiv_rn(v[2 * j], div), __fdiv_rn(v[2 * j + 1], div)) << (8 * j);
         }
     }
     return s;
+}
+__device__ __forceinline__ float amax4(const float* v) {
+    return fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 }
 
 // APPEND: heads are [q | k | v]; q to bf16 rows, k and v to the cache.  Otherwise [q | k] to rows of Y.
@@ -185,14 +166,17 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs
     const int kind = c < cq ? 0 : c < cq + ck ? 1 : 2;
     c -= kind == 0 ? 0 : kind == 1 ? cq : cq + ck;
     const int heads = kind == 0 ? a.Hq : a.Hkv, base = kind == 0 ? 0 : kind == 1 ? a.Hq : a.Hq + a.Hkv;
-    const int sub = lane / LPH, d0 = (lane % LPH) * 8;
-    const int h0 = c * kHeadsPerWarp + sub;            // heads h0, h0 + HPW, ..
-    const X* row = reinterpret_cast<const X*>(a.x) + t * a.ldx + (int64_t)base * D + d0;
+    const int sub = lane / LPH, l = lane % LPH;
+    const bool turn = kind < 2 && l < a.rot / 8;  // this lane's values are rotated
+    const bool split = !INTER && turn;            // its two runs lie half the rotated part apart
+    const int d0 = split ? 4 * l : 8 * l, d1 = split ? a.rot / 2 + 4 * l : 8 * l + 4;
+    const int h0 = c * kHeadsPerWarp + sub;  // heads h0, h0 + HPW, ..
+    const X* row = reinterpret_cast<const X*>(a.x) + t * a.ldx + (int64_t)base * D;
     Raw8<X> raw[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         if (h0 + i * HPW < heads)
-            raw[i].load(row + (int64_t)(h0 + i * HPW) * D);
+            raw[i].load(row + (int64_t)(h0 + i * HPW) * D, d0, d1);
         else
             raw[i].zero();
     }
@@ -201,8 +185,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs
     const int64_t pos = a.rot > 0 ? a.pos[t] : 0;
     const float* wp = kind == 0 ? a.qw : a.kw;
     const bool norm = kind < 2 && wp != nullptr;
-    float cs[8], sn[8], w[8];
-    if (norm) load8(wp + d0, w);
+    float cs[4], sn[4], w[8];
+    if (norm) {
+        Raw8<float> rw;
+        rw.load(wp, d0, d1);
+        rw.get(w);
+    }
     bool bad = a.rot > 0 && (pos < 0 || pos >= a.n_pos);
     if constexpr (APPEND) {
         if (slot == -1) return;
@@ -212,32 +200,50 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs
         if (lane == 0) atomicOr(a.status, kStatusBad);
         return;
     }
-    if (kind < 2 && d0 < a.rot) load_turn<INTER>(a.cs + pos * a.rot, a.rot, d0, cs, sn);
+    if (turn) load_turn<INTER>(a.cs + pos * a.rot, a.rot, d0, cs, sn);
     if (!APPEND || kind == 0) {
         Y* out = kind == 0 ? reinterpret_cast<Y*>(a.q) + t * a.ldq : reinterpret_cast<Y*>(a.k) + t * a.ldk;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float v[8];
             raw[i].get(v);
-            norm_rope<float, D, INTER>(v, norm, w, a.eps, a.rot, d0, cs, sn);
-            if (h0 + i * HPW < heads) store8(out + (int64_t)(h0 + i * HPW) * D + d0, v);
+            norm_rope<float, D, INTER>(v, norm, w, a.eps, turn, cs, sn);
+            if (h0 + i * HPW < heads) {
+                Y* dst = out + (int64_t)(h0 + i * HPW) * D;
+                store4(dst + d0, v);
+                store4(dst + d1, v + 4);
+            }
         }
     } else {
         const bool isv = kind == 2;
+        const float g = isv ? a.cache.v_scale : a.cache.k_scale;
         const int off = slot & ((1 << a.cache.page_log) - 1), r = off & 15;
-        const int code_at = isv ? v_code_off(D) + (d0 >> 4) * 128 + r * 8 + (d0 & 15) / 2 : r * (D / 2) + d0 / 2;
-        const int scale_at = isv ? v_scale_off(D) + (d0 >> 4) * 16 + r : k_scale_off(D) + r * (D / 16) + (d0 >> 4);
+        auto code_at = [&](int d) { return isv ? v_code_off(D) + (d >> 4) * 128 + r * 8 + (d & 15) / 2 : r * (D / 2) + d / 2; };
+        auto scale_at = [&](int d) { return isv ? v_scale_off(D) + (d >> 4) * 16 + r : k_scale_off(D) + r * (D / 16) + (d >> 4); };
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float v[8];
             raw[i].get(v);
-            if (!isv) norm_rope<double, D, INTER>(v, norm, w, a.eps, a.rot, d0, cs, sn);
-            uint32_t codes;
-            const uint8_t sc = quant8(v, isv ? a.cache.v_scale : a.cache.k_scale, codes);
+            if (!isv) norm_rope<double, D, INTER>(v, norm, w, a.eps, turn, cs, sn);
+            // a block of 16 values: both runs of two lanes, or one run of four
+            float m0 = amax4(v), m1 = amax4(v + 4);
+            if (!split) m0 = m1 = fmaxf(m0, m1);
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 1));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 1));
+            const float o0 = __shfl_xor_sync(0xffffffffu, m0, 2), o1 = __shfl_xor_sync(0xffffffffu, m1, 2);
+            if (split) m0 = fmaxf(m0, o0), m1 = fmaxf(m1, o1);
+            uint32_t c0, c1;
+            const uint8_t s0 = quant4(v, m0, g, c0), s1 = quant4(v + 4, m1, g, c1);
             if (h0 + i * HPW < heads) {
-                uint8_t* g = group_ptr<D>(a.cache, slot >> a.cache.page_log, h0 + i * HPW, off);
-                *reinterpret_cast<uint32_t*>(g + code_at) = codes;
-                if ((lane & 1) == 0) g[scale_at] = sc;
+                uint8_t* dst = group_ptr<D>(a.cache, slot >> a.cache.page_log, h0 + i * HPW, off);
+                if (split) {
+                    *reinterpret_cast<uint16_t*>(dst + code_at(d0)) = (uint16_t)c0;
+                    *reinterpret_cast<uint16_t*>(dst + code_at(d1)) = (uint16_t)c1;
+                    if ((l & 3) == 0) dst[scale_at(d0)] = s0, dst[scale_at(d1)] = s1;
+                } else {
+                    *reinterpret_cast<uint32_t*>(dst + code_at(d0)) = c0 | c1 << 16;
+                    if ((l & 1) == 0) dst[scale_at(d0)] = s0;
+                }
             }
         }
     }
