@@ -12,8 +12,12 @@
 namespace qlin {
 namespace kv {
 
+// Heads a warp.  What is only normed and rotated: 8, so that a token's row of the table and the weights are loaded once for
+// many (2048 tokens: 8.5 us, 9.8 with 4).  What is quantized: 4, for the path is long and its code repeated for each
+// (8192 tokens appended: 54 us, 73 with 8).
 constexpr int kHeadsPerWarp = 8;
-constexpr int kRopeWarps = 4;
+constexpr int kQuantHeadsPerWarp = 4;
+constexpr int kRopeWarps = 2;
 
 struct RopeArgs {
     const void* x;
@@ -124,28 +128,31 @@ __device__ __forceinline__ void norm_rope(float (&v)[8], bool norm, const float 
     for (int j = 0; j < 8; ++j) v[j] = (float)n[j];
 }
 
-// E2M1 codes of 4 values (2 bytes) of a block whose largest magnitude is m, and the block's scale byte, under scale g.
-__device__ __forceinline__ uint8_t quant4(const float* v, float m, float g, uint32_t& codes) {
-    const uint8_t s = e4m3_rne_sat(__fdiv_rn(m, __fmul_rn(6.0f, g)));
+// The scale byte of a block whose largest magnitude is m, under scale g: E4M3(m / (6 g)).  div_by_recip gives the correctly
+// rounded quotient where nothing over- or underflows on the way; g6 = 6 g and its reciprocal y6 are the same for all.
+__device__ __forceinline__ uint8_t block_scale(float m, float g6, float y6) {
+    const bool plain = g6 >= 0x1p-60f && g6 <= 0x1p60f && m <= 0x1p60f;
+    return e4m3_rne_sat(plain ? div_by_recip(m, g6, y6) : __fdiv_rn(m, g6));
+}
+// E2M1 codes (2 bytes a run) of N runs of 4 values under one scale byte; m bounds their magnitudes.
+template <int N>
+__device__ __forceinline__ void block_codes(const float* v, float m, uint8_t s, float g, uint32_t* codes) {
     const float div = __fmul_rn(e4m3_to_f32(s), g);
-    codes = 0u;
-    if (div > 0.f) {
-        // The reciprocal and its corrections give the correctly rounded quotient where nothing over- or underflows
-        // on the way (div_by_recip): ordinary scales, quotients below 2^60.
-        const float y = __frcp_rn(div);
-        if (div >= 0x1p-96f && div <= 0x1p96f && m * y <= 0x1p60f) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float2 qv = div_by_recip2(make_float2(v[2 * j], v[2 * j + 1]), div, y);
-                codes |= e2m1x2_rne_sat(qv.x, qv.y) << (8 * j);
-            }
-        } else {
+    for (int i = 0; i < N; ++i) codes[i] = 0u;
+    if (!(div > 0.f)) return;
+    const float y = __frcp_rn(div);
+    if (div >= 0x1p-96f && div <= 0x1p96f && m * y <= 0x1p60f) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                codes |= e2m1x2_rne_sat(__fdiv_rn(v[2 * j], div), __fdiv_rn(v[2 * j + 1], div)) << (8 * j);
+        for (int j = 0; j < 2 * N; ++j) {
+            const float2 qv = div_by_recip2(make_float2(v[2 * j], v[2 * j + 1]), div, y);
+            codes[j / 2] |= e2m1x2_rne_sat(qv.x, qv.y) << (8 * (j & 1));
         }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2 * N; ++j)
+            codes[j / 2] |= e2m1x2_rne_sat(__fdiv_rn(v[2 * j], div), __fdiv_rn(v[2 * j + 1], div)) << (8 * (j & 1));
     }
-    return s;
 }
 __device__ __forceinline__ float amax4(const float* v) {
     return fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
@@ -155,14 +162,14 @@ __device__ __forceinline__ float amax4(const float* v) {
 template <typename X, typename Y, int D, bool INTER, bool APPEND>
 __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs a) {
     constexpr int LPH = D / 8, HPW = 32 / LPH;         // lanes a head, heads a warp at once
-    constexpr int N = kHeadsPerWarp / HPW;             // heads a lane
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * kRopeWarps + warp;
     const int64_t t = item / a.chunks;
     if (t >= a.T) return;
     // this warp's heads: chunks of queries, then of keys, then of values
     int c = (int)(item - t * a.chunks);
-    const int cq = APPEND && !a.q ? 0 : (a.Hq + kHeadsPerWarp - 1) / kHeadsPerWarp, ck = (a.Hkv + kHeadsPerWarp - 1) / kHeadsPerWarp;
+    constexpr int KVH = APPEND ? kQuantHeadsPerWarp : kHeadsPerWarp;
+    const int cq = APPEND && !a.q ? 0 : (a.Hq + kHeadsPerWarp - 1) / kHeadsPerWarp, ck = (a.Hkv + KVH - 1) / KVH;
     const int kind = c < cq ? 0 : c < cq + ck ? 1 : 2;
     c -= kind == 0 ? 0 : kind == 1 ? cq : cq + ck;
     const int heads = kind == 0 ? a.Hq : a.Hkv, base = kind == 0 ? 0 : kind == 1 ? a.Hq : a.Hq + a.Hkv;
@@ -170,12 +177,13 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs
     const bool turn = kind < 2 && l < a.rot / 8;  // this lane's values are rotated
     const bool split = !INTER && turn;            // its two runs lie half the rotated part apart
     const int d0 = split ? 4 * l : 8 * l, d1 = split ? a.rot / 2 + 4 * l : 8 * l + 4;
-    const int h0 = c * kHeadsPerWarp + sub;  // heads h0, h0 + HPW, ..
+    const int h0 = c * (kind == 0 ? kHeadsPerWarp : KVH) + sub;  // heads h0, h0 + HPW, ..
     const X* row = reinterpret_cast<const X*>(a.x) + t * a.ldx + (int64_t)base * D;
+    constexpr int N = kHeadsPerWarp / HPW, NKV = KVH / HPW;  // heads a lane
     Raw8<X> raw[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        if (h0 + i * HPW < heads)
+        if (h0 + i * HPW < heads && (i < NKV || kind == 0))
             raw[i].load(row + (int64_t)(h0 + i * HPW) * D, d0, d1);
         else
             raw[i].zero();
@@ -216,24 +224,34 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs
         }
     } else {
         const bool isv = kind == 2;
-        const float g = isv ? a.cache.v_scale : a.cache.k_scale;
+        const float g = isv ? a.cache.v_scale : a.cache.k_scale, g6 = __fmul_rn(6.0f, g), y6 = __frcp_rn(g6);
         const int off = slot & ((1 << a.cache.page_log) - 1), r = off & 15;
         auto code_at = [&](int d) { return isv ? v_code_off(D) + (d >> 4) * 128 + r * 8 + (d & 15) / 2 : r * (D / 2) + d / 2; };
         auto scale_at = [&](int d) { return isv ? v_scale_off(D) + (d >> 4) * 16 + r : k_scale_off(D) + r * (D / 16) + (d >> 4); };
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < NKV; ++i) {
             float v[8];
             raw[i].get(v);
             if (!isv) norm_rope<double, D, INTER>(v, norm, w, a.eps, turn, cs, sn);
-            // a block of 16 values: both runs of two lanes, or one run of four
+            // a block of 16 values: both runs of two lanes, or one run of four (the same branch for all lanes but where a
+            // head is rotated in part)
             float m0 = amax4(v), m1 = amax4(v + 4);
             if (!split) m0 = m1 = fmaxf(m0, m1);
             m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 1));
             m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 1));
             const float o0 = __shfl_xor_sync(0xffffffffu, m0, 2), o1 = __shfl_xor_sync(0xffffffffu, m1, 2);
-            if (split) m0 = fmaxf(m0, o0), m1 = fmaxf(m1, o1);
-            uint32_t c0, c1;
-            const uint8_t s0 = quant4(v, m0, g, c0), s1 = quant4(v + 4, m1, g, c1);
+            uint32_t code[2];
+            uint8_t s0, s1;
+            if (split) {
+                m0 = fmaxf(m0, o0), m1 = fmaxf(m1, o1);
+                s0 = block_scale(m0, g6, y6), s1 = block_scale(m1, g6, y6);
+                block_codes<1>(v, m0, s0, g, code);
+                block_codes<1>(v + 4, m1, s1, g, code + 1);
+            } else {
+                s0 = s1 = block_scale(m0, g6, y6);
+                block_codes<2>(v, m0, s0, g, code);
+            }
+            const uint32_t c0 = code[0], c1 = code[1];
             if (h0 + i * HPW < heads) {
                 uint8_t* dst = group_ptr<D>(a.cache, slot >> a.cache.page_log, h0 + i * HPW, off);
                 if (split) {
@@ -309,8 +327,9 @@ extern "C" cudaError_t qlin_launch_qk_rope(const qlin_kv_cache* cache, const voi
                                            void* ws, cudaStream_t s) {
     kv::RopeArgs a = {};
     a.x = x, a.T = T, a.ldx = ldx, a.Hq = Hq, a.Hkv = Hkv;
-    const auto chunks = [](int heads) { return (heads + kv::kHeadsPerWarp - 1) / kv::kHeadsPerWarp; };
-    a.chunks = (cache && !q ? 0 : chunks(Hq)) + (cache ? 2 : 1) * chunks(Hkv);
+    const auto chunks = [](int heads, int per) { return (heads + per - 1) / per; };
+    a.chunks = cache ? (q ? chunks(Hq, kv::kHeadsPerWarp) : 0) + 2 * chunks(Hkv, kv::kQuantHeadsPerWarp)
+                     : chunks(Hq, kv::kHeadsPerWarp) + chunks(Hkv, kv::kHeadsPerWarp);
     a.qw = p->q_weight, a.kw = p->k_weight, a.cs = p->cos_sin, a.n_pos = p->n_pos, a.rot = p->rot, a.eps = p->eps;
     a.pos = positions, a.slots = slots, a.q = q, a.ldq = ldq, a.k = k, a.ldk = ldk;
     a.status = (unsigned*)ws;
