@@ -369,10 +369,6 @@ def qlin_gemv_chain(fmt, xdt, M, ops, flags=0, ws=None, stream=None):
 
 
 # ----------------------------------------------------------------------------- queries, keys and the 4-bit cache
-_XDT = {torch.float32: QLIN_F32, torch.bfloat16: QLIN_BF16}
-_YDT = {QLIN_F32: torch.float32, QLIN_BF16: torch.bfloat16}
-
-
 def qlin_kv_cache_bytes(n_pages, page, Hkv, D):
     return lib().qlin_kv_cache_bytes(n_pages, page, Hkv, D)
 
@@ -403,140 +399,66 @@ def kv_cache(n_pages, page, Hkv, D, k_scale=1.0, v_scale=1.0, device="cuda"):
     return KVCache(_alloc_aligned(nbytes, device).zero_(), page, Hkv, D, k_scale, v_scale)
 
 
-# A decode step makes these calls once a layer, so what the binding itself costs counts: device numbers instead of device
-# objects, the raw stream handle, and each argument looked at once.
-_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+# A decode step makes these calls once a layer, so their arguments are looked at in native code (csrc/torch_binding.cpp,
+# built beside the library): the checks and the C call take about 5 us, 13 to 17 through ctypes.
+_native = None
 
 
-def _ptr(t, name, dtype, index, shape=None):
-    """Address of a contiguous CUDA tensor on device `index` (None for None), its dtype and shape checked."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.get_device() != index:
-        raise TypeError(f"{name} must be a {dtype} tensor on cuda:{index}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+def _binding():
+    """The native binding, bound to the loaded library; raises if it is missing."""
+    global _native
+    l = lib()
+    with _lock:
+        if _native is None:
+            try:
+                from . import _qlin_torch
+            except ImportError as e:
+                raise RuntimeError(f"the native binding is not built in {_HERE} ({e}); run "
+                                   "`python -m gemm_dequant_gemv_q8_b200.build`") from e
+            _qlin_torch.bind(QlinError, *(ctypes.cast(getattr(l, n), _P).value for n in (
+                "qlin_qk_norm_rope", "qlin_kv_append", "qlin_kv_gather", "qlin_attn_kv4")))
+            _native = _qlin_torch
+    return _native
 
 
-def _rows(t, name, dtype, index, T, heads, D):
-    """(address, row stride) of T rows of heads * D contiguous values: (T, heads, D) or (T, heads * D)."""
-    if t.dtype is not dtype or t.get_device() != index:
-        raise TypeError(f"{name} must be a {dtype} tensor on cuda:{index}")
-    shape = t.shape
-    if shape != (T, heads, D) and shape != (T, heads * D):
-        raise ValueError(f"{name} must be ({T}, {heads}, {D}) or ({T}, {heads * D}), got {tuple(shape)}")
-    if t.is_contiguous():
-        return t.data_ptr(), heads * D
-    st = t.stride()
-    if (st[-1] != 1 and D > 1) or (len(st) == 3 and heads > 1 and st[1] != D):
-        raise ValueError(f"{name}'s rows must be contiguous")
-    return t.data_ptr(), st[0] if T > 1 else heads * D
-
-
-def _x_rows(x, width, exact):
-    """(dtype code, device, rows, row stride) of the projections' rows."""
-    xdt = _XDT.get(x.dtype)
-    if xdt is None or not x.is_cuda or x.dim() != 2:
-        raise TypeError("x must be a 2-d float32 or bfloat16 CUDA tensor")
-    T, W = x.shape
-    if W != width and (exact or W < width):
-        raise ValueError(f"x must have {'' if exact else 'at least '}{width} columns, got {W}")
-    ld = x.stride(0)
-    if x.stride(1) != 1:
-        raise ValueError("x rows must be contiguous")
-    return xdt, x.get_device(), T, ld if T > 1 else W
-
-
-def _ws(ws, nbytes, index):
-    """(address, bytes) of a workspace, a fresh one where none is given."""
-    if ws is None:
-        ws = workspace(nbytes, torch.device("cuda", index))
-    elif ws.get_device() != index or not ws.is_contiguous():
-        raise TypeError(f"ws must be a contiguous tensor on cuda:{index}")
-    return ws, ws.data_ptr(), ws.nbytes
-
-
-def _call(fn, index, stream, *args):
-    """fn(*args, stream) with device `index` current (the library works on the current device)."""
-    if stream is not None and stream.device_index != index:
+def _on(stream, index):
+    """Handle of a stream that has to be on device `index`."""
+    if stream.device_index != index:
         raise ValueError(f"the stream must be on cuda:{index}")
-    f = getattr(_lib or lib(), fn)
-    if _get_device() == index:
-        st = f(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
-    else:
-        with torch.cuda.device(index):
-            st = f(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
-    if st != 0:
-        raise QlinError(fn, st)
-
-
-def _qk_params(cos_sin, q_weight, k_weight, eps, rot, flags, D, index):
-    n_pos, table = 0, None
-    if cos_sin is None:
-        rot = 0
-    else:
-        if cos_sin.dim() != 2 or (rot is not None and rot and cos_sin.shape[1] != rot):
-            raise ValueError("cos_sin must be (positions, rot)")
-        n_pos, width = cos_sin.shape
-        rot = width if rot is None else rot
-        table = _ptr(cos_sin, "cos_sin", torch.float32, index)
-    return QKParams(_ptr(q_weight, "q_weight", torch.float32, index, (D,)), _ptr(k_weight, "k_weight", torch.float32, index, (D,)),
-                    table, n_pos, rot, flags, eps)
+    return stream.cuda_stream
 
 
 def qlin_qk_norm_rope(x, Hq, Hkv, D, positions=None, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, rot=None,
                       flags=QLIN_ROPE_HALVES, q=None, k=None, ydt=QLIN_BF16, ws=None, stream=None):
     """Norm (where a weight is given) and rotation of the query and key heads at the front of x's rows
     (T, >= (Hq + Hkv) * D).  Returns (q, k) as (T, heads, D); q and k may be x's own heads."""
-    xdt, dev, T, ldx = _x_rows(x, (Hq + Hkv) * D, False)
-    out = _YDT[ydt]
-    if q is None:
-        q = torch.empty((T, Hq, D), dtype=out, device=x.device)
-    if k is None:
-        k = torch.empty((T, Hkv, D), dtype=out, device=x.device)
-    pq, ldq = _rows(q, "q", out, dev, T, Hq, D)
-    pk, ldk = _rows(k, "k", out, dev, T, Hkv, D)
-    ws, pw, nw = _ws(ws, 256, dev)
-    par = _qk_params(cos_sin, q_weight, k_weight, eps, rot, flags, D, dev)
-    _call("qlin_qk_norm_rope", dev, stream, x.data_ptr(), xdt, T, ldx, Hq, Hkv, D, ctypes.addressof(par),
-          _ptr(positions, "positions", torch.int32, dev, (T,)), pq, ldq, pk, ldk, ydt, 0, pw, nw)
-    return q, k
+    if ws is None:
+        ws = workspace(256, x.device)
+    if stream is not None:
+        stream = _on(stream, x.get_device())
+    return (_native or _binding()).qk_norm_rope(x, Hq, Hkv, D, positions, cos_sin, q_weight, k_weight, eps, rot, flags, q, k,
+                                                ydt, ws, stream)
 
 
 def qlin_kv_append(cache, x, Hq, positions, slots, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, rot=None,
                    flags=QLIN_ROPE_HALVES, q=None, ws=None, stream=None):
     """Append the tokens of x's rows (T, (Hq + 2 Hkv) * D: [q | k | v], fp32 or bf16) to the cache at `slots`
     (int32; -1: a padding row).  Returns the normed and rotated queries, (T, Hq, D) bf16."""
-    Hkv, D = cache.Hkv, cache.D
-    xdt, dev, T, ldx = _x_rows(x, (Hq + 2 * Hkv) * D, True)
-    if cache.index != dev:
-        raise ValueError(f"the cache must be on cuda:{dev}")
-    if q is None:
-        q = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=x.device)
-    pq, ldq = _rows(q, "q", torch.bfloat16, dev, T, Hq, D) if Hq else (None, 0)
-    ws, pw, nw = _ws(ws, 256, dev)
-    par = _qk_params(cos_sin, q_weight, k_weight, eps, rot, flags, D, dev)
-    _call("qlin_kv_append", dev, stream, cache.ref, x.data_ptr(), xdt, T, ldx, Hq, ctypes.addressof(par),
-          _ptr(positions, "positions", torch.int32, dev, (T,)), _ptr(slots, "slots", torch.int32, dev, (T,)), pq, ldq, 0, pw, nw)
-    return q
+    if ws is None:
+        ws = workspace(256, cache.data.device)
+    if stream is not None:
+        stream = _on(stream, cache.index)
+    return (_native or _binding()).kv_append(cache.ref, cache.index, x, Hq, cache.Hkv, cache.D, positions, slots, cos_sin, q_weight,
+                                             k_weight, eps, rot, flags, q, ws, stream)
 
 
 def qlin_kv_gather(cache, slots, k=None, v=None, ydt=QLIN_BF16, ws=None, stream=None):
     """The values that slots of the cache stand for: (k, v), each (T, Hkv, D) fp32 or bf16."""
-    dev, out, shape = cache.index, _YDT[ydt], (slots.shape[0], cache.Hkv, cache.D)
-    if k is None:
-        k = torch.empty(shape, dtype=out, device=cache.data.device)
-    if v is None:
-        v = torch.empty(shape, dtype=out, device=cache.data.device)
-    ws, pw, nw = _ws(ws, 256, dev)
-    _call("qlin_kv_gather", dev, stream, cache.ref, shape[0], _ptr(slots, "slots", torch.int32, dev, shape[:1]),
-          _ptr(k, "k", out, dev, shape), _ptr(v, "v", out, dev, shape), ydt, pw, nw)
-    return k, v
+    if ws is None:
+        ws = workspace(256, cache.data.device)
+    if stream is not None:
+        stream = _on(stream, cache.index)
+    return (_native or _binding()).kv_gather(cache.ref, cache.index, slots, cache.Hkv, cache.D, k, v, ydt, ws, stream)
 
 
 def qlin_attn_kv4_workspace_bytes(cache, B, max_q, Hq):
@@ -547,21 +469,9 @@ def qlin_attn_kv4(cache, q, block_table, seq_lens, cu_q, max_q, scale=None, wind
     """Causal attention of B sequences' last tokens over the cache.  q: (total_q, Hq, D) bf16; block_table: (B,
     pages) int32; seq_lens: (B,) int32, each context with the call's own tokens; cu_q: (B + 1,) int32, the
     sequences' first rows of q; max_q: the most queries of one sequence.  Returns out, q's shape, bf16."""
-    dev, D, Bf = cache.index, cache.D, torch.bfloat16
-    if q.dim() != 3:
-        raise ValueError(f"q must be (total_q, Hq, {D})")
-    total, Hq, _ = q.shape
-    pq, ldq = _rows(q, "q", Bf, dev, total, Hq, D)
-    if out is None:
-        out = torch.empty((total, Hq, D), dtype=Bf, device=q.device)
-    po, ldo = _rows(out, "out", Bf, dev, total, Hq, D)
-    B = seq_lens.shape[0]
-    if (block_table.dtype is not torch.int32 or block_table.get_device() != dev or block_table.dim() != 2
-            or block_table.shape[0] != B or block_table.stride(1) != 1):
-        raise ValueError(f"block_table must be a ({B}, pages) int32 tensor on cuda:{dev} with contiguous rows")
-    pages = block_table.shape[1]
-    ws, pw, nw = _ws(ws, 0 if ws is not None else qlin_attn_kv4_workspace_bytes(cache, B, max_q, Hq), dev)
-    _call("qlin_attn_kv4", dev, stream, cache.ref, pq, ldq, block_table.data_ptr(), block_table.stride(0) if B > 1 else pages,
-          pages, _ptr(seq_lens, "seq_lens", torch.int32, dev, (B,)), _ptr(cu_q, "cu_q", torch.int32, dev, (B + 1,)), B, max_q,
-          total, Hq, D ** -0.5 if scale is None else scale, window, po, ldo, 0, pw, nw)
-    return out
+    if ws is None:
+        ws = workspace(qlin_attn_kv4_workspace_bytes(cache, seq_lens.shape[0], max_q, q.shape[1]), cache.data.device)
+    if stream is not None:
+        stream = _on(stream, cache.index)
+    return (_native or _binding()).attn_kv4(cache.ref, cache.index, cache.D, q, block_table, seq_lens, cu_q, max_q,
+                                            cache.D ** -0.5 if scale is None else scale, window, out, ws, stream)

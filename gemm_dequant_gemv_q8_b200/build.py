@@ -1,4 +1,5 @@
-"""Build libqlin.so (all CUDA sources of the package) for sm_100a with nvcc, in-tree.
+"""Build libqlin.so (all CUDA sources of the package) for sm_100a with nvcc, and the native binding
+_qlin_torch.so with g++ against the installed torch, in-tree.
 
 Usage: python -m gemm_dequant_gemv_q8_b200.build  [--force]
 """
@@ -19,6 +20,10 @@ FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std
          "-I", os.path.join(ROOT, "include")]
 
 
+BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
+BINDING = os.path.join(HERE, "_qlin_torch.so")
+
+
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
@@ -31,7 +36,28 @@ def _stale():
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_binding(force: bool = False) -> str:
+    """The argument marshalling of the cache's and the attention's calls (csrc/torch_binding.cpp)."""
+    deps = [BINDING_SRC, os.path.join(ROOT, "include", "qlin.h")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
+        return BINDING
+    import sysconfig
+
+    import torch
+    here = os.path.dirname(torch.__file__)
+    includes = [os.path.join(here, "include"), os.path.join(here, "include", "torch", "csrc", "api", "include"),
+                os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    subprocess.check_call([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+                           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                           *(a for p in includes for a in ("-isystem", p)), BINDING_SRC, "-o", tmp,
+                           "-L", os.path.join(here, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_binding(force)
     if not force and not _stale():
         return LIB
     objs = []
