@@ -12,6 +12,7 @@ struct AttnArgs {
     const int32_t *table, *lens, *cu;
     int64_t ldq, ldo, ldb, total_q;
     int max_pages, B, max_q, Hq, G;
+    uint32_t g_magic;  // ceil(2^32 / G), 0 for G = 1: rows to queries without a division (group_div)
     float scale_log2;  // scale * k_scale * log2(e)
     int window;        // 0: none; below 2^30
     unsigned* status;
@@ -19,6 +20,16 @@ struct AttnArgs {
     int* tickets;       // in the workspace: kMaxParts, zero between calls
     float* parts;       // then the parts of what several CTAs share
 };
+
+// r / G and r % G of a query row r < 2^26 (2^20 queries, G <= 64): r * (ceil(2^32 / G) - 2^32 / G) < 2^26 <= 2^32 / G, so
+// the high word of the product is the quotient.
+__device__ __forceinline__ int group_div(const AttnArgs& a, int r) { return a.g_magic ? (int)__umulhi((uint32_t)r, a.g_magic) : r; }
+__device__ __forceinline__ int group_mod(const AttnArgs& a, int r) { return r - group_div(a, r) * a.G; }
+// a / b, in 32 bits where both fit (the usual case by far).
+__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
+    if (((uint64_t)(a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
 
 constexpr int kMaxParts = 512;  // CTAs of a launch at most: tickets in the workspace
 

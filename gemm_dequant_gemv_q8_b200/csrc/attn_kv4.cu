@@ -27,10 +27,10 @@ namespace kv {
 template <int D, int NT>
 struct Dec {
     static constexpr int kWarps = NT == 1 ? 16 : 8;
-    static constexpr int kTile = D == 128 ? 32 : 64;      // tokens a stage
+    static constexpr int kTile = 32;  // tokens a stage
     static constexpr int kGroups = kTile / kGroup;
     static constexpr int kStageBytes = kGroups * group_bytes(D);
-    static constexpr int kStages = NT == 1 ? 3 : 5;
+    static constexpr int kStages = D == 128 ? (NT == 1 ? 3 : 5) : (NT == 1 ? 5 : 9);  // 147 KB in flight
     static constexpr int kRows = 8 * NT;
     static constexpr int kSteps = D / 16;  // k-steps of S, and 16-row tiles of O^T
     static constexpr int kPad = D + 8;     // floats a row of a warp's O in its stage buffer
@@ -45,7 +45,8 @@ constexpr int kMaxDecSeqs = 256;  // sequences of a launch
 static_assert(Dec<128, 1>::smem(kMaxDecSeqs) <= 232448 && Dec<64, 1>::smem(kMaxDecSeqs) <= 232448 &&
                   Dec<128, 2>::smem(kMaxDecSeqs) <= 232448 && Dec<64, 2>::smem(kMaxDecSeqs) <= 232448,
               "shared memory");
-static_assert(8 * Dec<128, 1>::kPad * 4 <= Dec<128, 1>::kStageBytes, "a warp's O of 8 rows fits a stage");
+static_assert(8 * Dec<128, 1>::kPad * 4 <= Dec<128, 1>::kStageBytes && 8 * Dec<64, 1>::kPad * 4 <= Dec<64, 1>::kStageBytes,
+              "a warp's O of 8 rows fits a stage");
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -74,6 +75,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
     uint32_t* source = reinterpret_cast<uint32_t*>(red + W * 8);  // [warp][32] the cache's groups that its next tiles are
     uint8_t* qbuf = reinterpret_cast<uint8_t*>(source + W * 32);  // [2] this segment's queries and the next one's
     int* flag = reinterpret_cast<int*>(qbuf + 2 * C::kQBytes);
+    int* longest = flag + 1;  // tiles of the longest sequence's segments
     int* prefix = flag + 4;  // [B + 1] tiles of one (head, row block) before sequence b
     int *row0 = prefix + a.B + 1, *length = row0 + a.B + 1;  // [B + 1] first rows of q, [B] contexts
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -81,7 +83,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
 
     if (lane < S) mbar_init(&bars[warp * S + lane], NG);
     if (warp == 0) {
-        int run = 0;
+        int run = 0, most = 0;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
             const int b = b0 + lane;
             int v = 0;
@@ -91,6 +93,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                 row0[b + 1] = (int)s.row0 + s.n, length[b] = s.L;
                 if (s.bad && blockIdx.x == 0) atomicOr(a.status, kStatusBad);
             }
+            most = max(most, v);
 #pragma unroll
             for (int k = 1; k < 32; k <<= 1) {
                 const int u = __shfl_up_sync(0xffffffffu, v, k);
@@ -99,7 +102,8 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
             if (b < a.B) prefix[b + 1] = run + v;
             run += __shfl_sync(0xffffffffu, v, 31);
         }
-        if (lane == 0) prefix[0] = 0, row0[0] = __ldg(a.cu);
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) prefix[0] = 0, row0[0] = __ldg(a.cu), *longest = most;
     }
     fence_mbar_init();
     __syncthreads();
@@ -115,13 +119,6 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         }
     }
 
-    // this CTA's range of tiles
-    const int64_t T = (int64_t)prefix[a.B] * HR;
-    const int64_t want = (T + a.min_tiles - 1) / a.min_tiles;
-    const int P = (int)(want < gridDim.x ? want : gridDim.x);
-    if ((int)blockIdx.x >= P) return;
-    const int64_t t0 = T * blockIdx.x / P, t1 = T * (blockIdx.x + 1) / P;
-
     auto locate = [&](int64_t tile) {
         Cursor c;
         int lo = 0, hi = a.B - 1;  // the last b with prefix[b] * HR <= tile (it has tiles)
@@ -133,10 +130,24 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         c.b = lo;
         c.per = prefix[lo + 1] - prefix[lo];
         const int64_t u = tile - (int64_t)prefix[lo] * HR;
-        c.hr = (int)(u / c.per);
+        c.hr = (int)div_small(u, c.per);
         c.i = (int)(u - (int64_t)c.hr * c.per);
         return c;
     };
+    // This CTA's range of tiles: the T-th parts of the list.  Where every segment is at most a tile a warp, the ranges
+    // end with segments: no parts to join between CTAs.
+    const int64_t T = (int64_t)prefix[a.B] * HR;
+    const bool whole_segs = *longest <= W;
+    const int64_t want = whole_segs ? (int64_t)a.B * HR : div_small(T + a.min_tiles - 1, a.min_tiles);
+    const int P = (int)(want < gridDim.x ? want : gridDim.x);
+    if ((int)blockIdx.x >= P || T == 0) return;
+    int64_t t0 = div_small(T * blockIdx.x, P), t1 = div_small(T * (blockIdx.x + 1), P);
+    if (whole_segs) {
+        t0 -= t0 < T ? locate(t0).i : 0;
+        t1 -= t1 < T ? locate(t1).i : 0;
+        if (t0 >= t1) return;
+    }
+
     auto queries = [&](int b) { return row0[b + 1] - row0[b]; };
     auto skip = [&](Cursor& c, int n) {  // n tiles on; the end of the list is not reached
         c.i += n;
@@ -203,8 +214,8 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         const int rr = c.hr % a.RB * C::kRows + qr;
         uint4 u = make_uint4(0, 0, 0, 0);
         if (qr < C::kRows && rr < queries(c.b) * a.G)
-            u = __ldg(reinterpret_cast<const uint4*>(a.q + ((int64_t)row0[c.b] + rr / a.G) * a.ldq +
-                                                     (int64_t)(c.hr / a.RB * a.G + rr % a.G) * D + qd));
+            u = __ldg(reinterpret_cast<const uint4*>(a.q + ((int64_t)row0[c.b] + group_div(a, rr)) * a.ldq +
+                                                     (int64_t)(c.hr / a.RB * a.G + group_mod(a, rr)) * D + qd));
         return u;
     };
     auto store_q = [&](const uint4& u, uint8_t* to) {
@@ -248,7 +259,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                 for (int c = 0; c < 2; ++c) {
                     const int r = nt * 8 + 2 * t + c;
                     rs[nt][c] = reinterpret_cast<const float*>(qs + C::kRows * D * 2)[r];
-                    hi[nt][c] = qL - qn + (rb * C::kRows + r) / a.G;  // the last place that the column's query sees
+                    hi[nt][c] = qL - qn + group_div(a, rb * C::kRows + r);  // the last place that the column's query sees
                     m[nt][c] = -INFINITY;
                     l[nt][c] = 0.f;
                 }
@@ -455,7 +466,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
             qnext = load_q(seg);
         }
         // join the warps' parts, 8 rows at a time, in the order of the warps
-        const int c0 = (int)(((s0 + 1) * P - 1) / T), c1 = (int)((s1 * P - 1) / T);
+        const int c0 = whole_segs ? 0 : (int)div_small((s0 + 1) * P - 1, T), c1 = whole_segs ? 0 : (int)div_small(s1 * P - 1, T);
         const bool whole = c0 == c1;
         float* part = a.parts + (int64_t)(2 * blockIdx.x + ((int)blockIdx.x == c0)) * C::kRows * (D + 2);
 #pragma unroll
@@ -504,8 +515,8 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                 if (whole) {
                     const float inv = sum > 0.f ? a.cache.v_scale / sum : 0.f;
                     const int rr = rb * C::kRows + nt * 8 + r;
-                    *reinterpret_cast<__nv_bfloat162*>(a.out + (qrow + rr / a.G) * a.ldo +
-                                                       (int64_t)(h * a.G + rr % a.G) * D + 2 * pair) =
+                    *reinterpret_cast<__nv_bfloat162*>(a.out + (qrow + group_div(a, rr)) * a.ldo +
+                                                       (int64_t)(h * a.G + group_mod(a, rr)) * D + 2 * pair) =
                         __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
                 } else {
                     __stcg(reinterpret_cast<float2*>(part + (nt * 8 + r) * D + 2 * pair), acc);
@@ -597,7 +608,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                     if (sp == 0 && r < rows) {
                         const float inv = sum > 0.f ? a.cache.v_scale / sum : 0.f;
                         const int rr = rb * C::kRows + r;
-                        __nv_bfloat16* dst = a.out + (qrow + rr / a.G) * a.ldo + (int64_t)(h * a.G + rr % a.G) * D + lane * V;
+                        __nv_bfloat16* dst = a.out + (qrow + group_div(a, rr)) * a.ldo + (int64_t)(h * a.G + group_mod(a, rr)) * D + lane * V;
 #pragma unroll
                         for (int k = 0; k < V; k += 2)
                             *reinterpret_cast<__nv_bfloat162*>(dst + k) = __floats2bfloat162_rn(acc[k] * inv, acc[k + 1] * inv);
@@ -676,6 +687,7 @@ extern "C" cudaError_t qlin_launch_attn_kv4(const qlin_kv_cache* c, const void* 
     a.q = (const __nv_bfloat16*)q, a.out = (__nv_bfloat16*)out;
     a.table = table, a.lens = lens, a.cu = cu, a.ldq = ldq, a.ldo = ldo, a.ldb = ldb, a.total_q = total_q;
     a.max_pages = max_pages, a.B = B, a.max_q = max_q, a.Hq = Hq, a.G = Hq / c->Hkv;
+    a.g_magic = a.G == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + a.G - 1) / a.G);
     a.scale_log2 = scale * c->k_scale * 1.4426950408889634f;
     a.window = window < (1 << 30) ? window : 0;  // no context is longer
     a.status = (unsigned*)ws;
