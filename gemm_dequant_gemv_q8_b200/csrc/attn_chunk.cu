@@ -10,9 +10,10 @@
 //   warps 8-11    : dequantize K, a token a thread, and V, 16 values x 8 tokens a thread, into 128-byte-swizzled K-major
 //                   tiles [token][value] and [value][token] in two stages each, with the next tile's codes on their way
 //                   into registers and the pages after that looked up;
-//   warp 12       : one thread issues the products: S_A, S_B, then per tile of tokens P V of A, the next S_A, P V of B, the
-//                   next S_B, so that the tensor cores work for one tile while the other's softmax runs
-//                   (warps 13-15 are idle: registers are dealt out by four warps).
+//   warp 12       : issues the products, S_A, S_B, then per tile of tokens P V of A, the next S_A, P V of B, the
+//                   next S_B: the tensor cores work for one tile while the other's softmax runs;
+//   warp 13       : deals out the units: a ring of descriptions in shared memory that the others read
+//                   (warps 14 and 15 are idle: registers are dealt out by four warps).
 // The exponent's reference follows the running maximum only when that has grown by 2^8, so O is rarely rescaled.
 // Units are dealt out heaviest first, there and back; those of the last, partial round are split along the tokens
 // where that shortens it, and the last CTA of a unit to finish joins its parts in their order.
@@ -29,17 +30,22 @@ namespace ch {
 constexpr int kRows = 256, kTok = 128;
 constexpr int kSoftWarps = 8, kDqWarps = 4, kMmaWarp = kSoftWarps + kDqWarps;
 constexpr int kThreads = (kMmaWarp + 4) * 32;
-// Registers a thread: 128 at launch (512 threads), then by role; the softmax warps' share comes from the idle ones'.
-constexpr int kSoftRegs = 152, kDqRegs = 128, kMmaRegs = 72;
-static_assert(256 * kSoftRegs + 128 * kDqRegs + 128 * kMmaRegs <= 512 * 128, "the launch's registers");
+// Registers a thread: 128 at launch (512 threads), then by role.  The softmax warps wait for what the others give back, so
+// every other role has its dec, and the shares add up to the launch's at most.
+constexpr int kSoftRegs = 152, kDqRegs = 112, kMmaRegs = 96;
+static_assert(kDqRegs < 128 && kMmaRegs < 128 && 256 * kSoftRegs + 128 * kDqRegs + 128 * kMmaRegs <= 512 * 128,
+              "the launch's registers");
 constexpr int kMaxSeqs = 1024;
-constexpr int kSplitCost = 3;  // tiles that a split's queries, rows and joining cost
+constexpr int kItems = 4;      // descriptions in the ring
+// What a unit costs beside its tiles, and what joining its parts does, in tiles (2.4 us): queries in and rows out; the parts'
+// way through the workspace; reading one (131 KB at what an SM gets).
+constexpr float kUnitCost = 2.f, kJoinCost = 1.5f, kPartCost = 0.3f;
 
 template <int D>
 struct Cfg {
     static constexpr int kQBytes = 128 * D * 2;  // one tile of queries
     static constexpr int kKBytes = kTok * D * 2, kVBytes = kTok * D * 2;
-    static constexpr int kSmem = 1024 + 2 * kQBytes + 2 * kKBytes + 2 * kVBytes + 512 + (kMmaWarp + 1) * 64;
+    static constexpr int kSmem = 1024 + 2 * kQBytes + 2 * kKBytes + 2 * kVBytes + 512 + kItems * 64;
     static constexpr int smem(int B) { return kSmem + (3 * B + 2) * 4; }
 };
 static_assert(Cfg<128>::smem(kMaxSeqs) <= 232448, "shared memory");
@@ -113,7 +119,6 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
         : "memory");
 }
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // A piece of work: 256 rows of one (sequence, kv head) from row `base`, tiles [t0, t1) of 128 tokens.
 struct Item {
@@ -142,27 +147,30 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 21);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     int* last_flag = reinterpret_cast<int*>(tmem_holder + 2);
-    int* tail_tiles = reinterpret_cast<int*>(tmem_holder + 3);  // of all units of the last round
-    Item* slots = reinterpret_cast<Item*>(bars + 64);     // [warp] the piece of work it is at
-    int* prefix = reinterpret_cast<int*>(slots + kMmaWarp + 1);  // [B + 1] units of one kv head before sequence b
+    uint64_t *itemfull = bars + 24, *itemfree = itemfull + kItems, *softbar = itemfree + kItems;
+    Item* ring = reinterpret_cast<Item*>(bars + 64);
+    int* prefix = reinterpret_cast<int*>(ring + kItems);  // [B + 1] units of one kv head before sequence b
     int *row0 = prefix + a.B + 1, *length = row0 + a.B + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int Hkv = a.cache.Hkv;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&qfull[i], 128);
+            mbar_init(&qfull[i], 4);
             mbar_init(&kfull[i], kDqWarps * 32);
             mbar_init(&vfull[i], kDqWarps * 32);
             mbar_init(&kfree[i], 1);
             mbar_init(&vfree[i], 1);
             mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[i], 128);
+            mbar_init(&pfull[i], 4);
             mbar_init(&ofull[i], 1);
         }
         mbar_init(mma_done, 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&itemfull[i], 1);
+            mbar_init(&itemfree[i], kSoftWarps + kDqWarps + 1);
+        }
+        mbar_init(softbar, kSoftWarps);
         *abort_flag = 0;
-        *tail_tiles = 0;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -195,73 +203,6 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
     fence_after();
     const uint32_t tmem = *tmem_holder;
 
-    // unit u: sequences in order; in each the last rows first (the most tokens), the kv heads of a block side by side
-    auto unit = [&](int u) {
-        Item it;
-        int lo = 0, hi = a.B - 1;  // the last b with prefix[b] * Hkv <= u (it has units)
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if ((int64_t)prefix[mid] * Hkv <= u) lo = mid;
-            else hi = mid - 1;
-        }
-        const int k = u - prefix[lo] * Hkv, blocks = prefix[lo + 1] - prefix[lo];
-        it.b = lo;
-        it.h = k % Hkv;
-        it.base = (blocks - 1 - k / Hkv) * kRows;
-        it.n = row0[lo + 1] - row0[lo];
-        it.L = length[lo];
-        it.row0 = row0[lo];
-        it.rows = min(kRows, it.n * a.G - it.base);
-        const int p0 = it.L - it.n + it.base / a.G, p1 = it.L - it.n + (it.base + it.rows - 1) / a.G;
-        const int first = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
-        it.t0 = first / kTok;
-        it.t1 = p1 < 0 ? it.t0 : p1 / kTok + 1;
-        it.part = 0, it.parts = 1, it.tail = -1;
-        return it;
-    };
-    const int64_t units64 = (int64_t)prefix[a.B] * Hkv;
-    const int units = (int)units64;
-    const int grid = gridDim.x, whole = units / grid * grid, tails = units - whole;
-    // splits of the last round's units: their rounds times a part's tiles and its fixed cost, the least of it
-    for (int i = threadIdx.x; i < tails; i += kThreads) {
-        const Item it = unit(whole + i);
-        atomicAdd(tail_tiles, it.t1 - it.t0);
-    }
-    __syncthreads();
-    int splits = 1;
-    if (tails > 0) {
-        const float avg = (float)*tail_tiles / tails;
-        float best = avg + kSplitCost;
-        for (int s = 2; s <= 32 && tails * s <= 2 * grid; ++s) {
-            const float cost = (float)((tails * s + grid - 1) / grid) * (avg / s + kSplitCost) + kSplitCost;
-            if (cost < best && avg >= 2 * s) best = cost, splits = s;
-        }
-    }
-    const int items = whole + tails * splits;
-    auto item = [&](int k) {  // the k-th of this CTA: rounds go there and back
-        const int i = k * grid + ((k & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
-        if (i >= items) {
-            Item none = {};
-            none.b = -1;
-            return none;
-        }
-        if (i < whole || splits == 1) return unit(i);
-        const int r = (i - whole) / splits, s = (i - whole) % splits;
-        Item it = unit(whole + r);
-        const int cnt = it.t1 - it.t0, first = it.t0;
-        it.t0 = first + (int)((int64_t)cnt * s / splits);
-        it.t1 = first + (int)((int64_t)cnt * (s + 1) / splits);
-        it.part = s, it.parts = splits, it.tail = r;
-        return it;
-    };
-    const int rounds = (items + grid - 1) / grid;
-    // A warp's k-th piece of work, in its slot: what a role does not need at the moment takes no register.
-    auto take = [&](int k) -> const Item& {
-        __syncwarp();
-        if (lane == 0) slots[warp] = item(k);
-        __syncwarp();
-        return slots[warp];
-    };
     auto wait = [&](uint64_t* bar, int parity) {  // false: gave up, or another warp has
         if (*abort_flag) return false;
         if (mbar_wait_bounded(bar, parity)) return true;
@@ -269,6 +210,14 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
         *abort_flag = 1;
         return false;
     };
+    auto warp_wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    auto warp_arrive = [&](uint64_t* bar) {
+        __syncwarp();
+        if (lane == 0) arrive(bar);
+    };
+    // A role's k-th piece of work; false at the end.  done(k) gives its place in the ring back.
+    auto take = [&](int k) { return warp_wait(&itemfull[k % kItems], (k / kItems) & 1) && ring[k % kItems].b >= 0; };
+    auto done_with = [&](int k) { warp_arrive(&itemfree[k % kItems]); };
 
     if (warp < kSoftWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -277,24 +226,28 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
         const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + 256 + x * D;
         uint8_t* qx = qt + x * C::kQBytes;
         int tiles = 0, its = 0;  // of this tile of rows so far: the barriers' phases
-        bool ok = true;          // after a wait that gave up: no more products, but every barrier of the eight warps
-        auto warp_wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+        int soft_syncs = 0;
+        bool ok = true;          // after a wait that gave up: no more work
         int all_tiles = 0;       // of the CTA: the bad groups' ring
-        for (int k = 0; k < rounds; ++k) {
-            const Item& it = take(k);
-            if (it.b < 0) continue;
+        auto soft_sync = [&]() {  // the eight warps
+            warp_arrive(softbar);
+            ok = warp_wait(softbar, soft_syncs & 1) && ok;
+            ++soft_syncs;
+        };
+        for (int k = 0; ok && take(k); done_with(k), ++k) {
+            const Item& it = ring[k % kItems];
             const int cnt = it.t1 - it.t0, first = it.t0;
-            const int p = it.L - it.n + (it.base + srow) / a.G;  // the last place this row sees
+            const int p = it.L - it.n + group_div(a, it.base + srow);  // the last place this row sees
             // of this warp's rows: the first one's and the last one's
-            const int pw0 = it.L - it.n + (it.base + x * 128 + quarter * 32) / a.G;
-            const int pw1 = it.L - it.n + (it.base + x * 128 + quarter * 32 + 31) / a.G;
+            const int pw0 = it.L - it.n + group_div(a, it.base + x * 128 + quarter * 32);
+            const int pw1 = it.L - it.n + group_div(a, it.base + x * 128 + quarter * 32 + 31);
             float rs = 0.f, m = -INFINITY, l = 0.f;
-            const bool active = x * 128 < it.rows && cnt > 0 && ok;
+            const bool active = x * 128 < it.rows && cnt > 0;
             if (active) {
                 // This warp's 32 rows of queries as fp16, 16-byte pieces of 128-byte rows turned by the row: D / 8 lanes a row,
                 // so that a load is whole rows.
                 constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows a load
-#pragma unroll
+#pragma unroll 1
                 for (int h0 = 0; h0 < 32; h0 += 8 * RPI) {
                     uint4 u[8];
 #pragma unroll
@@ -302,8 +255,8 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                         const int wr = quarter * 32 + h0 + i * RPI + lane / LPR, rr = it.base + x * 128 + wr;
                         u[i] = make_uint4(0, 0, 0, 0);
                         if (x * 128 + wr < it.rows)
-                            u[i] = __ldg(reinterpret_cast<const uint4*>(a.q + (it.row0 + rr / a.G) * a.ldq +
-                                                                        (int64_t)(it.h * a.G + rr % a.G) * D) + lane % LPR);
+                            u[i] = __ldg(reinterpret_cast<const uint4*>(a.q + (it.row0 + group_div(a, rr)) * a.ldq +
+                                                                        (int64_t)(it.h * a.G + group_mod(a, rr)) * D) + lane % LPR);
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -321,7 +274,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                     }
                 }
                 fence_proxy_async_smem();
-                arrive(&qfull[x]);
+                warp_arrive(&qfull[x]);
                 for (int j = 0; j < cnt; ++j) {
                     ok = warp_wait(&sfull[x], tiles & 1);
                     if (!ok) break;
@@ -436,7 +389,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                     l += sum.x + sum.y;
                     st_wait();
                     fence_before();
-                    arrive(&pfull[x]);
+                    warp_arrive(&pfull[x]);
                 }
                 ok = ok && warp_wait(&ofull[x], its & 1);
                 ++its;
@@ -449,7 +402,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             const int64_t slot = it.parts > 1 ? (int64_t)(it.tail * it.parts + it.part) : 0;
             float* part = a.parts + slot * kRows * (D + 2);  // [D / 4][256 rows] of four values, then [256] {m, l}
             const float inv = l > 0.f ? a.cache.v_scale / l : 0.f;
-            __nv_bfloat16* dst = a.out + (it.row0 + r / a.G) * a.ldo + (int64_t)(it.h * a.G + r % a.G) * D;
+            __nv_bfloat16* dst = a.out + (it.row0 + group_div(a, r)) * a.ldo + (int64_t)(it.h * a.G + group_mod(a, r)) * D;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float v[32];
@@ -495,27 +448,44 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                 }
                 soft_sync();
                 if (*last_flag && valid) {
-                    const float* base = a.parts + (int64_t)it.tail * it.parts * kRows * (D + 2);
+                    // Each row its own thread.  The parts' factors wait in the queries' place, which nothing reads any
+                    // more; the sums come four parts at a time.
+                    const int64_t psz = (int64_t)kRows * (D + 2);
+                    const float* base = a.parts + (int64_t)it.tail * it.parts * psz;
+                    auto ml_of = [&](int s) { return __ldcg(reinterpret_cast<const float2*>(base + s * psz + (int64_t)kRows * D) + srow); };
+                    float* factor = reinterpret_cast<float*>(qt) + srow;
                     float mj = -INFINITY, lj = 0.f;
-                    for (int s = 0; s < it.parts; ++s)
-                        mj = fmaxf(mj, __ldcg(reinterpret_cast<const float2*>(base + (int64_t)s * kRows * (D + 2) + (int64_t)kRows * D) + srow).x);
+#pragma unroll 8
+                    for (int s = 0; s < it.parts; ++s) mj = fmaxf(mj, ml_of(s).x);
                     const float ref = mj == -INFINITY ? 0.f : mj;
+#pragma unroll 8
                     for (int s = 0; s < it.parts; ++s) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(base + (int64_t)s * kRows * (D + 2) + (int64_t)kRows * D) + srow);
-                        lj += ml.y * ex2(ml.x - ref);
+                        const float2 ml = ml_of(s);
+                        const float f = ex2(ml.x - ref);
+                        factor[s * kRows] = f;
+                        lj += ml.y * f;
                     }
                     const float invj = lj > 0.f ? a.cache.v_scale / lj : 0.f;
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
                         float4 acc[4] = {};
-                        for (int s = 0; s < it.parts; ++s) {
-                            const float* ps = base + (int64_t)s * kRows * (D + 2);
-                            const float f = ex2(__ldcg(reinterpret_cast<const float2*>(ps + (int64_t)kRows * D) + srow).x - ref);
+                        for (int s0 = 0; s0 < it.parts; s0 += 4) {
+                            float4 v[4][4];
+                            float f[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float4 v = __ldcg(reinterpret_cast<const float4*>(ps) + (c / 4 + i) * kRows + srow);
-                                acc[i].x += f * v.x, acc[i].y += f * v.y, acc[i].z += f * v.z, acc[i].w += f * v.w;
+                            for (int u = 0; u < 4; ++u) {
+                                const int s = s0 + u < it.parts ? s0 + u : it.parts - 1;
+                                f[u] = s0 + u < it.parts ? factor[s * kRows] : 0.f;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    v[u][i] = __ldcg(reinterpret_cast<const float4*>(base + s * psz) + (c / 4 + i) * kRows + srow);
                             }
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    acc[i].x += f[u] * v[u][i].x, acc[i].y += f[u] * v[u][i].y, acc[i].z += f[u] * v[u][i].z,
+                                        acc[i].w += f[u] * v[u][i].w;
                         }
                         uint32_t u[8];
 #pragma unroll
@@ -532,18 +502,19 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             }
         }
     } else if (warp < kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDqRegs));
         const int id = threadIdx.x - kSoftWarps * 32;  // 0 .. 127
         // K: token id of the tile.  V: 16 values, block id / 16, of 8 tokens from 8 (id % 16)
         const int vblk = id >> 4, vch = id & 15;
         const bool vuse = vblk < D / 16;
         constexpr int KW = D / 8, KS = D / 64;  // words of codes and of scales of a token's K
-        int k = 0;
+        int k = -1;
         auto next_item = [&]() {  // the next one that has tokens
-            while (k < rounds) {
-                const Item& to = take(k++);
-                if (to.b >= 0 && to.t1 > to.t0) return true;
+            for (;;) {
+                if (k >= 0) done_with(k);
+                if (!take(++k)) return false;
+                if (ring[k % kItems].t1 > ring[k % kItems].t0) return true;
             }
-            return false;
         };
         // a tile that this thread has looked up: the groups of its tokens, or NULL (behind the end, a bad page)
         struct Place {
@@ -551,10 +522,10 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             int left;  // tokens from V's first one to the context's end
             bool bad, some;
         };
-        const Item& it = slots[warp];
         bool more = next_item();
-        int tile = more ? it.t0 - 1 : 0;
+        int tile = more ? ring[k % kItems].t0 - 1 : 0;
         auto group = [&](int tok, bool& bad_page) -> const uint8_t* {
+            const Item& it = ring[k % kItems];
             if (tok >= it.L) return nullptr;
             const int page = __ldg(a.table + it.b * a.ldb + (tok >> a.cache.page_log));
             if (page < 0 || page >= a.cache.n_pages) {
@@ -566,16 +537,16 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
         };
         auto step = [&]() {  // on to the next tile
             Place pl = {nullptr, nullptr, 0, false, false};
-            if (more && ++tile >= it.t1) {
+            if (more && ++tile >= ring[k % kItems].t1) {
                 more = next_item();
-                tile = it.t0;
+                tile = more ? ring[k % kItems].t0 : 0;
             }
             if (!more) return pl;
             bool ignored = false;
             pl.some = true;
             pl.k = group(tile * kTok + id, pl.bad);
             pl.v = vuse ? group(tile * kTok + vch * 8, ignored) : nullptr;
-            pl.left = it.L - (tile * kTok + vch * 8);
+            pl.left = ring[k % kItems].L - (tile * kTok + vch * 8);
             return pl;
         };
         struct Codes {
@@ -622,7 +593,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             Codes nc;
             fetch(next, nc);
             const Place ahead = step();
-            if (tiles >= 2 && !wait(&kfree[s], ((tiles >> 1) - 1) & 1)) break;
+            if (tiles >= 2 && !warp_wait(&kfree[s], ((tiles >> 1) - 1) & 1)) break;
             {
                 uint8_t* dst = kt + s * C::kKBytes + id * 128;
 #pragma unroll
@@ -642,7 +613,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             }
             fence_proxy_async_smem();
             arrive(&kfull[s]);
-            if (tiles >= 2 && !wait(&vfree[s], ((tiles >> 1) - 1) & 1)) break;
+            if (tiles >= 2 && !warp_wait(&vfree[s], ((tiles >> 1) - 1) & 1)) break;
             if (vuse) {
                 uint8_t* dst = vt + s * C::kVBytes + (vch >> 3) * (D * 128);
                 const uint32_t f[4] = {e4m3x2_to_f16x2(c.vs[0] & 0xffffu), e4m3x2_to_f16x2(c.vs[0] >> 16),
@@ -681,7 +652,6 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             bool ok = true;
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const uint32_t dq = desc_lo(smem_u32(qt)), dk = desc_lo(smem_u32(kt)), dv = desc_lo(smem_u32(vt));
-            auto warp_wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
             auto scores = [&](int x, int s) {
                 const uint32_t qa = dq + x * (C::kQBytes >> 4), ka = dk + s * (C::kKBytes >> 4), d = tm + x * 128;
 #pragma unroll
@@ -691,10 +661,10 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                 }
                 commit(&sfull[x]);
             };
-            for (int k = 0; k < rounds && ok; ++k) {
-                const Item& it = take(k);
-                if (it.b < 0 || it.t1 <= it.t0) continue;
-                const int cnt = it.t1 - it.t0, two = it.rows > 128 ? 2 : 1;
+            for (int k = 0; ok && take(k); ++k) {
+                const int cnt = ring[k % kItems].t1 - ring[k % kItems].t0, two = ring[k % kItems].rows > 128 ? 2 : 1;
+                done_with(k);
+                if (cnt <= 0) continue;
                 for (int x = 0; x < two && ok; ++x) {
                     ok = warp_wait(&qfull[x], q_its[x] & 1);
                     ++q_its[x];
@@ -733,6 +703,71 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             }
             commit(mma_done);  // every tensor-core operation of this warp is done before the teardown
             if (!mbar_wait_bounded(mma_done, 0)) atomicOr(a.status, 1u);
+        } else if (warp == kMmaWarp + 1) {
+            // unit u: sequences in order; in each the last rows first (the most tokens), the kv heads of a block side by side
+            auto unit = [&](int u) {
+                Item it;
+                int lo = 0, hi = a.B - 1;  // the last b with prefix[b] * a.cache.Hkv <= u (it has units)
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if ((int64_t)prefix[mid] * a.cache.Hkv <= u) lo = mid;
+                    else hi = mid - 1;
+                }
+                const int k = u - prefix[lo] * a.cache.Hkv, blocks = prefix[lo + 1] - prefix[lo];
+                it.b = lo;
+                it.h = k % a.cache.Hkv;
+                it.base = (blocks - 1 - k / a.cache.Hkv) * kRows;
+                it.n = row0[lo + 1] - row0[lo];
+                it.L = length[lo];
+                it.row0 = row0[lo];
+                it.rows = min(kRows, it.n * a.G - it.base);
+                const int p0 = it.L - it.n + group_div(a, it.base), p1 = it.L - it.n + group_div(a, it.base + it.rows - 1);
+                const int first = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
+                it.t0 = first / kTok;
+                it.t1 = p1 < 0 ? it.t0 : p1 / kTok + 1;
+                it.part = 0, it.parts = 1, it.tail = -1;
+                return it;
+            };
+            const int units = prefix[a.B] * a.cache.Hkv;
+            const int grid = gridDim.x, whole = units / grid * grid, tails = units - whole;
+            // splits of the last round's units: their rounds times a part's tiles and its fixed cost, the least of it
+            int splits = 1;
+            if (tails > 0) {
+                int sum = 0;
+                for (int i = lane; i < tails; i += 32) {
+                    const Item it = unit(whole + i);
+                    sum += it.t1 - it.t0;
+                }
+                sum = __reduce_add_sync(0xffffffffu, sum);
+                const float avg = (float)sum / tails;
+                float best = avg + kUnitCost;
+                for (int s = 2; s <= 32 && tails * s <= 2 * grid; ++s) {
+                    const float cost = (float)((tails * s + grid - 1) / grid) * (avg / s + kUnitCost) + kJoinCost + kPartCost * s;
+                    if (cost < best && avg >= 2 * s) best = cost, splits = s;
+                }
+            }
+            const int items = whole + tails * splits;
+            bool more = true;
+            for (int k = 0; more; ++k) {
+                // rounds go there and back
+                const int i = k * grid + ((k & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
+                Item it = {};
+                it.b = -1;
+                if (i < whole || (i < items && splits == 1)) {
+                    it = unit(i);
+                } else if (i < items) {
+                    const int r = (i - whole) / splits, s = (i - whole) % splits;
+                    it = unit(whole + r);
+                    const int cnt = it.t1 - it.t0, first = it.t0;
+                    it.t0 = first + (int)((int64_t)cnt * s / splits);
+                    it.t1 = first + (int)((int64_t)cnt * (s + 1) / splits);
+                    it.part = s, it.parts = splits, it.tail = r;
+                }
+                more = it.b >= 0;  // only the last round has places without work
+                if (k >= kItems && !warp_wait(&itemfree[k % kItems], (k / kItems - 1) & 1)) break;
+                if (lane == 0) ring[k % kItems] = it;
+                warp_arrive(&itemfull[k % kItems]);
+            }
         }
     }
     fence_before();
