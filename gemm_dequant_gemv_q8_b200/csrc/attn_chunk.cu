@@ -27,7 +27,8 @@ namespace kv {
 
 namespace ch {
 
-constexpr int kRows = 256, kTok = 128;
+constexpr int kRows = 256, kTok = 128;  // rows of a unit at most, tokens of a tile
+
 constexpr int kSoftWarps = 8, kDqWarps = 4, kMmaWarp = kSoftWarps + kDqWarps;
 constexpr int kThreads = (kMmaWarp + 4) * 32;
 // Registers a thread: 128 at launch (512 threads), then by role.  The softmax warps wait for what the others give back, so
@@ -147,7 +148,8 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 21);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     int* last_flag = reinterpret_cast<int*>(tmem_holder + 2);
-    uint64_t *itemfull = bars + 24, *itemfree = itemfull + kItems, *softbar = itemfree + kItems;
+    int* unit_rows = last_flag + 1;
+    uint64_t *itemfull = bars + 28, *itemfree = itemfull + kItems, *softbar = itemfree + kItems;
     Item* ring = reinterpret_cast<Item*>(bars + 64);
     int* prefix = reinterpret_cast<int*>(ring + kItems);  // [B + 1] units of one kv head before sequence b
     int *row0 = prefix + a.B + 1, *length = row0 + a.B + 1;
@@ -178,13 +180,22 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (warp == 0) {
+        // Where units of 256 rows would leave half of the SMs without one, units of one tile of rows.
+        int big = 0;
+        for (int b = lane; b < a.B; b += 32) {
+            const Seq s = seq_of(a, b);
+            if (!s.bad) big += (int)(((int64_t)s.n * a.G + kRows - 1) / kRows);
+        }
+        big = __reduce_add_sync(0xffffffffu, big);
+        const int ur = (int64_t)big * a.cache.Hkv * 2 <= gridDim.x ? kRows / 2 : kRows;
+        if (lane == 0) *unit_rows = ur;
         int run = 0;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
             const int b = b0 + lane;
             int v = 0;
             if (b < a.B) {
                 const Seq s = seq_of(a, b);
-                if (!s.bad) v = (int)(((int64_t)s.n * a.G + kRows - 1) / kRows);
+                if (!s.bad) v = (int)(((int64_t)s.n * a.G + ur - 1) / ur);
                 row0[b + 1] = (int)s.row0 + s.n, length[b] = s.L;
                 if (s.bad && blockIdx.x == 0) atomicOr(a.status, kStatusBad);
             }
@@ -283,9 +294,12 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                     const int tok0 = (first + j) * kTok;
                     const uint64_t out = *reinterpret_cast<const volatile uint64_t*>(bad + ((all_tiles + j) & 3) * 8);
                     const bool edge = out != 0 || tok0 + kTok - 1 > pw0 || (a.window > 0 && tok0 <= pw1 - a.window);
-                    auto sees = [&](int i) {  // whether this row sees the tile's token i
-                        const int tk = tok0 + i;
-                        return tk <= p && (a.window == 0 || tk > p - a.window) && !((out >> (8 * (i >> 4))) & 1);
+                    auto seen = [&](int c) {  // which of tokens 32 c .. 32 c + 31 of the tile this row sees
+                        const int last = p - tok0 - 32 * c, before = a.window > 0 ? last - a.window : -1;  // before < t <= last
+                        uint32_t b = last >= 31 ? 0xffffffffu : last < 0 ? 0u : (2u << last) - 1u;
+                        b &= before >= 31 ? 0u : before < 0 ? 0xffffffffu : ~((2u << before) - 1u);
+                        if (out != 0) b &= ~(((out >> (16 * c)) & 1 ? 0xffffu : 0u) | ((out >> (16 * c + 8)) & 1 ? 0xffff0000u : 0u));
+                        return b;
                     };
                     // 32 scores at a time, the next ones on their way while these are worked on.  (Loops of two such steps
                     // and not of all four: the roles' code shares the instruction cache.)
@@ -296,8 +310,9 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                         for (int c = 0; c < 4; ++c) {
                             ld32(ts + 32 * c, u0);
                             ld_wait(u0);
+                            const uint32_t b = seen(c);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) top = fmaxf(top, sees(32 * c + i) ? __uint_as_float(u0[i]) : -INFINITY);
+                            for (int i = 0; i < 32; ++i) top = fmaxf(top, (b >> i) & 1 ? __uint_as_float(u0[i]) : -INFINITY);
                         }
                     } else {
                         ld32(ts, u0);
@@ -351,12 +366,13 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                             uint32_t pk[16];
                             ld32(ts + 32 * c, u0);
                             ld_wait(u0);
+                            const uint32_t b = seen(c);
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) {
                                 float2 e2 = make_float2(ex2(__fsub_rn(__fmul_rn(__uint_as_float(u0[i]), rs), ref)),
                                                         ex2(__fsub_rn(__fmul_rn(__uint_as_float(u0[i + 1]), rs), ref)));
-                                e2.x = sees(32 * c + i) ? e2.x : 0.f;
-                                e2.y = sees(32 * c + i + 1) ? e2.y : 0.f;
+                                e2.x = (b >> i) & 1 ? e2.x : 0.f;
+                                e2.y = (b >> (i + 1)) & 1 ? e2.y : 0.f;
                                 sum = __fadd2_rn(sum, e2);
                                 pk[i / 2] = pack_f16x2(e2.x, e2.y);
                             }
@@ -716,11 +732,11 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                 const int k = u - prefix[lo] * a.cache.Hkv, blocks = prefix[lo + 1] - prefix[lo];
                 it.b = lo;
                 it.h = k % a.cache.Hkv;
-                it.base = (blocks - 1 - k / a.cache.Hkv) * kRows;
+                it.base = (blocks - 1 - k / a.cache.Hkv) * *unit_rows;
                 it.n = row0[lo + 1] - row0[lo];
                 it.L = length[lo];
                 it.row0 = row0[lo];
-                it.rows = min(kRows, it.n * a.G - it.base);
+                it.rows = min(*unit_rows, it.n * a.G - it.base);
                 const int p0 = it.L - it.n + group_div(a, it.base), p1 = it.L - it.n + group_div(a, it.base + it.rows - 1);
                 const int first = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
                 it.t0 = first / kTok;
