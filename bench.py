@@ -868,6 +868,63 @@ CONFIGS = {"q8_small": cfg_q8_small, "nvfp4_mlp": cfg_mlp, "moe": cfg_moe, "chun
            "moe_prefill": cfg_moe_prefill, "mxfp4_mlp": lambda a, cpu=True: cfg_mlp(a, "mxfp4", cpu)}
 
 
+def cfg_attn_step(args):
+    """A decode step of the default stack with its attention, M sequences of 4096 tokens of context: per layer the qkv
+    projection, the append of its rows to the layer's NVFP4 cache (norm and rotation on the way), the attention over
+    it, the o projection of the attention's output, then gate_up + SiLU and down.  qkv and gate_up read their own
+    seeded activations, as in the default workload; o reads the attention and down reads h."""
+    import gemm_dequant_gemv_q8_b200 as q
+    fmt, Hq, Hkv, D, page, L = q.QLIN_Q4_0, 32, 8, 128, 16, 4096
+    per, out = -(-L // page), {}
+    i = torch.arange(D // 2, device="cuda", dtype=torch.float64)
+    ang = torch.arange(L, device="cuda", dtype=torch.float64)[:, None] * 1e6 ** (-2 * i / D)
+    cos_sin = torch.cat([ang.cos(), ang.sin()], 1).float()
+    w = torch.ones(D, device="cuda")
+    for M in (1, 8):
+        stack = DenseStack(fmt, args.layers, M=M, mode="launches")
+        caches = []
+        for l in range(args.layers):
+            c = q.kv_cache(M * per, page, Hkv, D)
+            for b in range(M):  # the earlier tokens of each sequence
+                x = synth.activations(L, 6144, synth.gen(synth.seed_for(9, l, b), device="cuda"), device="cuda")
+                slots = torch.arange(L, device="cuda", dtype=torch.int32) + b * per * page
+                q.qlin_kv_append(c, x, Hq, torch.arange(L, device="cuda", dtype=torch.int32), slots, cos_sin, w, w)
+            caches.append(c)
+        table = torch.arange(M * per, device="cuda", dtype=torch.int32).view(M, per)
+        pos = torch.full((M,), L - 1, device="cuda", dtype=torch.int32)
+        slots = (torch.arange(M, device="cuda") * per * page + L - 1).int()
+        lens, cu = torch.full((M,), L, device="cuda", dtype=torch.int32), torch.arange(M + 1, device="cuda", dtype=torch.int32)
+        ws, wa = q.workspace(256), q.workspace(q.qlin_attn_kv4_workspace_bytes(caches[0], M, 1, Hq))
+        qo = torch.empty(M, Hq, D, dtype=torch.bfloat16, device="cuda")
+        ao = torch.empty_like(qo)
+
+        def attention(l):
+            q.qlin_kv_append(caches[l], stack.y[(l, 0)], Hq, pos, slots, cos_sin, w, w, q=qo, ws=ws)
+            q.qlin_attn_kv4(caches[l], qo, table, lens, cu, 1, out=ao, ws=wa)
+
+        def step():
+            for l in range(args.layers):
+                for pi, (_, N, K, epi) in enumerate(STACK):
+                    if pi == 1:
+                        attention(l)
+                    q.qlin_gemv(fmt, stack.packed[l][pi], N, K, ao.view(M, Hq * D) if pi == 1 else stack.x[(l, pi)],
+                                y=stack.y[(l, pi)], flags=q.QLIN_EPI_SILU_GATE if epi else q.QLIN_EPI_NONE, ws=stack.ws[l][pi])
+
+        ms, clk = timed(step, args.steps, args.warmup)
+        ams, _ = timed(lambda: [attention(l) for l in range(args.layers)], args.steps, args.warmup)
+        kv = args.layers * M * L * Hkv * D * 9 // 8
+        bytes_ = stack.step_bytes + kv
+        out[f"attn_step_m{M}"] = dict(
+            workload=f"Q4_0 dense decode step with attention over an NVFP4 cache, {M} sequences of {L} tokens ({args.layers} "
+                     "layers of hidden 2560, 32 query and 8 key / value heads of 128; six launches a layer)",
+            M=M, ms_per_step=ms, attention_ms_per_step=ams, cache_bytes=kv, packed_weight_bytes=stack.weight_bytes,
+            value=bytes_ / (ms * 1e-3) / 1e9, unit="GB/s", decode_tok_s=M * 1e3 / ms,
+            roofline=roofline_hbm("qk_rope_kernel + attn_decode_kernel, all layers", kv, ams * 1e3), clocks=clk,
+            l2="inputs larger than L2: %.2f GB of weights and cache per step" % (bytes_ / 1e9))
+        del stack, caches
+    return out
+
+
 def run_config(name, args):
     """Measure one workload other than the default stack; one JSON line per entry."""
     import gemm_dequant_gemv_q8_b200 as q
@@ -889,6 +946,8 @@ def run_config(name, args):
                              roofline=roofline_hbm(f"chain_kernel<{fname}, M=1>", stack.step_bytes, ms * 1e3),
                              clocks=clk,
                              l2="inputs larger than L2: %.2f GB of packed weights per step" % (stack.weight_bytes / 1e9))
+    elif name == "attn_step":
+        entries = cfg_attn_step(args)
     elif name == "gguf_chunk":
         # GGUF prefill chunk: the bf16 copy of dequantized Q4_0 weights (QLIN_PACK_MMA) times bf16 x on
         # the tensor cores (kind::f16), at the NVFP4 chunk workload's shape
@@ -1059,7 +1118,7 @@ def main():
                          "previous one's output (reported as an extra field either way)")
     ap.add_argument("--config", default="stack",
                     choices=["stack", "q8_small", "nvfp4_mlp", "mxfp4_mlp", "moe", "moe_prefill", "chunk", "q4_k_stack",
-                             "q6_k_stack", "gguf_chunk"],
+                             "q6_k_stack", "gguf_chunk", "attn_step"],
                     help="stack (default): the Q4_0 36-layer decode stack line; the others print their "
                          "entries alone")
     ap.add_argument("--small-case", choices=["moe1", "moe8", "mlp1", "mlp4", "moepf512", "chunk512"],

@@ -40,7 +40,6 @@ struct Dec {
     static constexpr int kFixed = kRing + kWarps * kStages * 16 + kWarps * 8 * 8 + kWarps * 32 * 4 + 2 * kQBytes + 16;
     static constexpr int smem(int B) { return kFixed + (3 * B + 2) * 4; }
 };
-constexpr int kFewRows = 64;      // rows of one (sequence, kv head) that this kernel takes at most
 constexpr int kMaxDecSeqs = 256;  // sequences of a launch
 static_assert(Dec<128, 1>::smem(kMaxDecSeqs) <= 232448 && Dec<64, 1>::smem(kMaxDecSeqs) <= 232448 &&
                   Dec<128, 2>::smem(kMaxDecSeqs) <= 232448 && Dec<64, 2>::smem(kMaxDecSeqs) <= 232448,
@@ -645,11 +644,18 @@ static int kv_sm_count() {
     return cached[dev];
 }
 
+// Whether the kernel for few rows takes a call.  It goes over the cache once for every 16 query rows of a kv head, but
+// spreads any context over all SMs; the one for chunks goes over it once for 256, in units of at least 128 rows.  us, few
+// rows against chunks: 1 x 8000 tokens (8 kv heads) 64 rows 28 / 47, 128 rows 38 / 49; 8 x 2000 32 rows 27 / 34, 64 rows
+// 41 / 34; 32 x 4000 32 rows 117 / 167, 64 rows 216 / 168.
+static bool few_rows(int64_t rows, int B, int Hkv) {
+    return rows <= 32 || (rows <= 128 && rows * B * Hkv <= 2048);
+}
+
 extern "C" size_t qlin_attn_kv4_ws_bytes(const qlin_kv_cache* c, int B, int max_q, int Hq) {
-    (void)B;
     const int64_t rows = (int64_t)max_q * (Hq / c->Hkv);
     const size_t fixed = 256 + kv::kMaxParts * 4;
-    if (rows > kv::kFewRows) return fixed + qlin_attn_chunk_part_bytes(c->D, kv_sm_count());
+    if (!few_rows(rows, B, c->Hkv)) return fixed + qlin_attn_chunk_part_bytes(c->D, kv_sm_count());
     return fixed + (size_t)2 * kv_sm_count() * (rows <= 8 ? 8 : 16) * (c->D + 2) * 4;
 }
 
@@ -695,7 +701,7 @@ extern "C" cudaError_t qlin_launch_attn_kv4(const qlin_kv_cache* c, const void* 
     a.parts = (float*)((uint8_t*)ws + 256 + kv::kMaxParts * 4);
     a.min_tiles = 8;
     const int64_t rows = (int64_t)max_q * a.G;
-    if (rows > kv::kFewRows) return qlin_launch_attn_chunk(&a, c->D, kv_sm_count(), s);
+    if (!few_rows(rows, B, c->Hkv)) return qlin_launch_attn_chunk(&a, c->D, kv_sm_count(), s);
     a.RB = rows <= 8 ? 1 : (int)((rows + 15) / 16);
     if (c->D == 128) return rows <= 8 ? launch_decode<128, 1>(a, s) : launch_decode<128, 2>(a, s);
     return rows <= 8 ? launch_decode<64, 1>(a, s) : launch_decode<64, 2>(a, s);
