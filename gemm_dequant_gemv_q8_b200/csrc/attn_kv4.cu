@@ -53,6 +53,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {  // C = 0
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -164,11 +170,11 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
 
     // this warp's tiles: t0 + warp, t0 + warp + W, ..
     int mine = t1 - t0 > warp ? (int)((t1 - t0 - warp + W - 1) / W) : 0;
-    int issued = 0;
+    int issued = 0, istage = 0;
     uint8_t* ring = smem + warp * S * C::kStageBytes;
     const unsigned heads_groups = (unsigned)a.cache.Hkv << (a.cache.page_log - 4);
     auto issue = [&]() {  // lane j copies group j of the next tile
-        const int s = issued % S, e = issued % C::kBatch;
+        const int s = istage, e = issued % C::kBatch;
         if (e == 0) {
             // where the next kBatch tiles lie, a group a lane: the searches and the page table's latency once for all
             uint32_t src = 0xffffffffu;  // behind the end, or a bad page: not copied, and masked
@@ -199,11 +205,11 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         }
         __syncwarp();
         ++issued;
+        istage = istage == S - 1 ? 0 : istage + 1;
     };
-    Cursor seg = locate(t0), cc = seg;
-    if (mine > 0) skip(cc, warp);
+    Cursor seg = locate(t0);
     int64_t s0 = t0 - seg.i;  // the first tile of this (sequence, head, row block)
-    int done = 0;
+    int done = 0, stage = 0, phase = 0;
     bool failed = false;
     // The queries of a segment go to shared memory as fp16 (row_exponent).  A row's D / 8 lanes hold 8 values each; lane
     // (g, t) of a product later reads its values (D / 4) t + 8 w .. + 7 of row g as one 16 bytes.
@@ -250,7 +256,12 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         float rs[NT][2], m[NT][2], l[NT][2];  // rs takes the scores to the exponents of 2
         int hi[NT][2];
         float o[KS][NT][4];
-        const bool any = done < mine && cc.b == seg.b && cc.hr == seg.hr;
+        // this warp's tiles of the segment: every W-th from `next`
+        const int64_t next = t0 + warp + (int64_t)done * W, end = s1 < t1 ? s1 : t1;
+        const int tiles = next < end ? (int)((end - next + W - 1) / W) : 0;
+        const bool any = tiles > 0;
+        float nref[NT][2];  // what is added to the exponents: -m, 0 where nothing has been seen
+        bool huge = false;  // some |m| of the warp is 2^24 or more
         if (any) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -260,7 +271,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                     rs[nt][c] = reinterpret_cast<const float*>(qs + C::kRows * D * 2)[r];
                     hi[nt][c] = qL - qn + group_div(a, rb * C::kRows + r);  // the last place that the column's query sees
                     m[nt][c] = -INFINITY;
-                    l[nt][c] = 0.f;
+                    l[nt][c] = nref[nt][c] = 0.f;
                 }
 #pragma unroll
             for (int i = 0; i < KS; ++i)
@@ -269,15 +280,16 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
 #pragma unroll
                     for (int c = 0; c < 4; ++c) o[i][nt][c] = 0.f;
         }
-        while (done < mine && cc.b == seg.b && cc.hr == seg.hr) {
-            const int s = done % S;
-            if (!mbar_wait_bounded(&bars[warp * S + s], (done / S) & 1, failed ? 50000000ull : 2000000000ull)) {
+        int tok0 = (tile0 + (int)(next - s0)) * TILE;
+        for (int j = 0; j < tiles; ++j, tok0 += W * TILE) {
+            const int s = stage;
+            if (failed && done >= issued) break;
+            if (!mbar_wait_bounded(&bars[warp * S + s], phase, failed ? 50000000ull : 2000000000ull)) {
                 if (lane == 0) atomicOr(a.status, 1u);
                 failed = true;
                 mine = issued;  // nothing more is copied; what is in flight is waited for
             }
             const uint8_t* st = ring + s * C::kStageBytes;
-            const int tok0 = (tile0 + cc.i) * TILE;
             const uint32_t bad = bad_groups[warp * S + s];
             // every row sees all of the tile's tokens, unless the tile reaches past the first row's place or
             // before the last one's window: the common form has no masks at all
@@ -292,7 +304,8 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                 for (int gr = 0; gr < NG; ++gr) {
                     const uint8_t* gp = st + gr * group_bytes(D);
                     if constexpr (D == 128) {
-                        const uint4 x = lds128(gp + ta * 64 + t * 16), y = lds128(gp + (ta + 2) * 64 + t * 16);
+                        const uint4 x = *reinterpret_cast<const uint4*>(gp + ta * 64 + t * 16);
+                        const uint4 y = *reinterpret_cast<const uint4*>(gp + (ta + 2) * 64 + t * 16);
                         w0[gr][0] = x.x, w0[gr][1] = x.y, w0[gr][2] = x.z, w0[gr][3] = x.w;
                         w1[gr][0] = y.x, w1[gr][1] = y.y, w1[gr][2] = y.z, w1[gr][3] = y.w;
                         const uint32_t z0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(gp + k_scale_off(D) + ta * 8 + t * 2));
@@ -308,16 +321,12 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                                                            (uint32_t)gp[k_scale_off(D) + (ta + 2) * 4 + t] << 8);
                         f0[gr][0] = __byte_perm(z, 0, 0x1010), f1[gr][0] = __byte_perm(z, 0, 0x3232);
                     }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) sc[gr][nt][c] = 0.f;
                 }
 #pragma unroll
                 for (int w = 0; w < WK; ++w) {  // a word of codes: two steps of the inner axis
                     uint4 qf[NT];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) qf[nt] = lds128(qs + ((w * C::kRows + nt * 8 + g) * 4 + t) * 16);
+                    for (int nt = 0; nt < NT; ++nt) qf[nt] = *reinterpret_cast<const uint4*>(qs + ((w * C::kRows + nt * 8 + g) * 4 + t) * 16);
 #pragma unroll
                     for (int gr = 0; gr < NG; ++gr) {
                         uint32_t h0[4], h1[4];
@@ -328,7 +337,10 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                         const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma16816(sc[gr][nt], a0, qf[nt].x, qf[nt].y);
+                            if (w == 0)
+                                mma16816_zero(sc[gr][nt], a0, qf[nt].x, qf[nt].y);
+                            else
+                                mma16816(sc[gr][nt], a0, qf[nt].x, qf[nt].y);
                             mma16816(sc[gr][nt], a1, qf[nt].z, qf[nt].w);
                         }
                     }
@@ -346,35 +358,37 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                                 sc[gr][nt][c] = sees ? sc[gr][nt][c] : -INFINITY;
                             }
                 }
-                float mx[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float v = -INFINITY;
-#pragma unroll
-                        for (int gr = 0; gr < NG; ++gr) v = fmaxf(v, fmaxf(sc[gr][nt][c], sc[gr][nt][2 + c]));
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                        mx[nt][c] = v == -INFINITY ? v : __fmul_rn(v, rs[nt][c]);
-                    }
                 // The reference that is taken off the scores follows the maximum only when that has grown by 2^8: the
-                // probabilities then reach 2^8, which fp16 holds, and O is rescaled rarely.
+                // probabilities then reach 2^8, which fp16 holds; the maximum goes round the lanes, and O is rescaled,
+                // only then.
+                float mx[NT][2];
                 bool grow = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) grow |= mx[nt][c] > m[nt][c] + 8.f;
+                    for (int c = 0; c < 2; ++c) {
+                        float v = fmaxf(sc[0][nt][c], sc[0][nt][2 + c]);
+#pragma unroll
+                        for (int gr = 1; gr < NG; ++gr) v = fmaxf(v, fmaxf(sc[gr][nt][c], sc[gr][nt][2 + c]));
+                        mx[nt][c] = v;
+                        grow |= __fmul_rn(v, rs[nt][c]) > m[nt][c] + 8.f;
+                    }
                 if (__any_sync(0xffffffffu, grow)) {
+                    bool big = false;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float f[2];
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const float mn = fmaxf(m[nt][c], mx[nt][c]);
+                            float v = mx[nt][c];
+                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                            const float mn = fmaxf(m[nt][c], v == -INFINITY ? v : __fmul_rn(v, rs[nt][c]));
                             f[c] = m[nt][c] == -INFINITY ? 0.f : ex2(m[nt][c] - mn);
                             m[nt][c] = mn;
+                            nref[nt][c] = mn == -INFINITY ? 0.f : -mn;
+                            big |= fabsf(nref[nt][c]) >= 0x1p24f;
                             l[nt][c] *= f[c];
                         }
 #pragma unroll
@@ -382,30 +396,41 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
 #pragma unroll
                             for (int c = 0; c < 4; ++c) o[i][nt][c] *= f[c & 1];
                     }
+                    huge = __any_sync(0xffffffffu, big);
+                }
+                // One rounding leaves up to half an ulp of the reference on the largest score's exponent, less than 1 below
+                // 2^24, the same for the whole row; beyond that two, as the reference has, make it 0.
+                float p[NG][NT][4];
+                if (edge || huge) {
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const float e = ex2(__fadd_rn(__fmul_rn(sc[gr][nt][c], rs[nt][c & 1]), nref[nt][c & 1]));
+                                p[gr][nt][c] = sc[gr][nt][c] == -INFINITY ? 0.f : e;  // also where rs is 0
+                            }
+                } else {
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) p[gr][nt][c] = ex2(fmaf(sc[gr][nt][c], rs[nt][c & 1], nref[nt][c & 1]));
                 }
                 uint32_t pf[NG][NT][2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float ref[2];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) ref[c] = m[nt][c] == -INFINITY ? 0.f : -m[nt][c];
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int gr = 0; gr < NG; ++gr) {
-                        float p[4];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)  // two roundings as in mx: the largest score's exponent is then 0, not a remainder
-                            p[c] = ex2(__fadd_rn(__fmul_rn(sc[gr][nt][c], rs[nt][c & 1]), ref[c & 1]));
-                        if constexpr (edge) {  // also where rs is 0
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) p[c] = sc[gr][nt][c] == -INFINITY ? 0.f : p[c];
-                        }
-                        l[nt][0] += p[0] + p[2];
-                        l[nt][1] += p[1] + p[3];
+                        const float* e = p[gr][nt];
+                        l[nt][0] += e[0] + e[2];
+                        l[nt][1] += e[1] + e[3];
                         // tokens to rows, heads to columns: the transpose is the operand that P V takes
-                        pf[gr][nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
-                        pf[gr][nt][1] = transpose8x8(pack_f16x2(p[2], p[3]));
+                        pf[gr][nt][0] = transpose8x8(pack_f16x2(e[0], e[1]));
+                        pf[gr][nt][1] = transpose8x8(pack_f16x2(e[2], e[3]));
                     }
-                }
                 // O^T: this lane's tokens of a group are 4 t .. 4 t + 3; row g (g + 8) of tile i is its value 2 i (2 i + 1)
                 // of D / 8 neighbouring values
 #pragma unroll
@@ -415,8 +440,8 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                     const int blk = D == 128 ? g : g >> 1;
                     uint32_t v[4][VW];
                     if constexpr (D == 128) {
-                        const uint4 x = lds128(gp + v_code_off(D) + blk * 128 + t * 32);
-                        const uint4 y = lds128(gp + v_code_off(D) + blk * 128 + t * 32 + 16);
+                        const uint4 x = *reinterpret_cast<const uint4*>(gp + v_code_off(D) + blk * 128 + t * 32);
+                        const uint4 y = *reinterpret_cast<const uint4*>(gp + v_code_off(D) + blk * 128 + t * 32 + 16);
                         v[0][0] = x.x, v[0][1] = x.y, v[1][0] = x.z, v[1][1] = x.w;
                         v[2][0] = y.x, v[2][1] = y.y, v[3][0] = y.z, v[3][1] = y.w;
                     } else {
@@ -452,7 +477,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
             else
                 step(cuda::std::false_type());
             ++done;
-            if (done < mine) skip(cc, W);
+            if (++stage == S) stage = 0, phase ^= 1;
             __syncwarp();
             if (issued < mine) issue();  // into the stage that was read before this one
         }
@@ -470,7 +495,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         float* part = a.parts + (int64_t)(2 * blockIdx.x + ((int)blockIdx.x == c0)) * C::kRows * (D + 2);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float* mo = reinterpret_cast<float*>(ring + ((done + S - 1) % S) * C::kStageBytes);
+            float* mo = reinterpret_cast<float*>(ring + (stage ? stage - 1 : S - 1) * C::kStageBytes);
             if (any) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -489,7 +514,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                 red[warp * 8 + lane] = make_float2(-INFINITY, 0.f);
             }
             // where each warp's buffer lies: a warp without a tile of its own is not read
-            if (lane == 0) bad_groups[W * S + warp] = (uint32_t)((done + S - 1) % S);
+            if (lane == 0) bad_groups[W * S + warp] = (uint32_t)(stage ? stage - 1 : S - 1);
             __syncthreads();
             for (int e = threadIdx.x; e < 8 * D / 2; e += W * 32) {
                 const int r = e / (D / 2), pair = e % (D / 2);
@@ -542,7 +567,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                 int rp = 1;
                 while (rp < rows && rp < W) rp *= 2;
                 const int nsp = W / rp, sp = warp / rp;
-                float* mo = reinterpret_cast<float*>(ring + ((done + S - 1) % S) * C::kStageBytes);
+                float* mo = reinterpret_cast<float*>(ring + (stage ? stage - 1 : S - 1) * C::kStageBytes);
                 for (int r = warp % rp; r < C::kRows; r += rp) {
                     float M = -INFINITY, sum = 0.f, acc[V];
 #pragma unroll
