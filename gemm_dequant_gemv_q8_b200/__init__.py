@@ -421,44 +421,45 @@ def _binding():
     return _native
 
 
-def _on(stream, index):
-    """Handle of a stream that has to be on device `index`."""
-    if stream.device_index != index:
-        raise ValueError(f"the stream must be on cuda:{index}")
-    return stream.cuda_stream
+def _on(stream, device, fn, *args):
+    """fn(*args) with `stream` current: what the call allocates belongs to that stream."""
+    if stream.device != device:
+        raise ValueError(f"the stream must be on {device}")
+    with torch.cuda.stream(stream):
+        return fn(*args)
 
 
 def qlin_qk_norm_rope(x, Hq, Hkv, D, positions=None, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, rot=None,
                       flags=QLIN_ROPE_HALVES, q=None, k=None, ydt=QLIN_BF16, ws=None, stream=None):
     """Norm (where a weight is given) and rotation of the query and key heads at the front of x's rows
     (T, >= (Hq + Hkv) * D).  Returns (q, k) as (T, heads, D); q and k may be x's own heads."""
+    if stream is not None:
+        return _on(stream, x.device, qlin_qk_norm_rope, x, Hq, Hkv, D, positions, cos_sin, q_weight, k_weight, eps, rot, flags, q, k, ydt, ws)
     if ws is None:
         ws = workspace(256, x.device)
-    if stream is not None:
-        stream = _on(stream, x.get_device())
     return (_native or _binding()).qk_norm_rope(x, Hq, Hkv, D, positions, cos_sin, q_weight, k_weight, eps, rot, flags, q, k,
-                                                ydt, ws, stream)
+                                                ydt, ws)
 
 
 def qlin_kv_append(cache, x, Hq, positions, slots, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, rot=None,
                    flags=QLIN_ROPE_HALVES, q=None, ws=None, stream=None):
     """Append the tokens of x's rows (T, (Hq + 2 Hkv) * D: [q | k | v], fp32 or bf16) to the cache at `slots`
     (int32; -1: a padding row).  Returns the normed and rotated queries, (T, Hq, D) bf16."""
+    if stream is not None:
+        return _on(stream, cache.data.device, qlin_kv_append, cache, x, Hq, positions, slots, cos_sin, q_weight, k_weight, eps, rot, flags, q, ws)
     if ws is None:
         ws = workspace(256, cache.data.device)
-    if stream is not None:
-        stream = _on(stream, cache.index)
     return (_native or _binding()).kv_append(cache.ref, cache.index, x, Hq, cache.Hkv, cache.D, positions, slots, cos_sin, q_weight,
-                                             k_weight, eps, rot, flags, q, ws, stream)
+                                             k_weight, eps, rot, flags, q, ws)
 
 
 def qlin_kv_gather(cache, slots, k=None, v=None, ydt=QLIN_BF16, ws=None, stream=None):
     """The values that slots of the cache stand for: (k, v), each (T, Hkv, D) fp32 or bf16."""
+    if stream is not None:
+        return _on(stream, cache.data.device, qlin_kv_gather, cache, slots, k, v, ydt, ws)
     if ws is None:
         ws = workspace(256, cache.data.device)
-    if stream is not None:
-        stream = _on(stream, cache.index)
-    return (_native or _binding()).kv_gather(cache.ref, cache.index, slots, cache.Hkv, cache.D, k, v, ydt, ws, stream)
+    return (_native or _binding()).kv_gather(cache.ref, cache.index, slots, cache.Hkv, cache.D, k, v, ydt, ws)
 
 
 def qlin_attn_kv4_workspace_bytes(cache, B, max_q, Hq):
@@ -469,9 +470,9 @@ def qlin_attn_kv4(cache, q, block_table, seq_lens, cu_q, max_q, scale=None, wind
     """Causal attention of B sequences' last tokens over the cache.  q: (total_q, Hq, D) bf16; block_table: (B,
     pages) int32; seq_lens: (B,) int32, each context with the call's own tokens; cu_q: (B + 1,) int32, the
     sequences' first rows of q; max_q: the most queries of one sequence.  Returns out, q's shape, bf16."""
+    if stream is not None:
+        return _on(stream, cache.data.device, qlin_attn_kv4, cache, q, block_table, seq_lens, cu_q, max_q, scale, window, out, ws)
     if ws is None:
         ws = workspace(qlin_attn_kv4_workspace_bytes(cache, seq_lens.shape[0], max_q, q.shape[1]), cache.data.device)
-    if stream is not None:
-        stream = _on(stream, cache.index)
     return (_native or _binding()).attn_kv4(cache.ref, cache.index, cache.D, q, block_table, seq_lens, cu_q, max_q,
-                                            cache.D ** -0.5 if scale is None else scale, window, out, ws, stream)
+                                            cache.D ** -0.5 if scale is None else scale, window, out, ws)

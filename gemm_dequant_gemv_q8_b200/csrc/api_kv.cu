@@ -22,6 +22,7 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 20;
 constexpr int64_t kMaxLd = (int64_t)1 << 31;
 constexpr int kMaxHeads = 1024;
 constexpr int kMaxSeqs = 1024;
+constexpr int64_t kMaxContext = (int64_t)1 << 26;  // a block table's tokens: tiles are counted in 32 bits
 constexpr int kMaxGroup = 64;  // query heads a kv head
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -148,10 +149,10 @@ qlin_status_t qlin_attn_kv4(const qlin_kv_cache* cache, const void* q, int64_t l
                             int max_q, int64_t total_q, int Hq, float scale, int window, void* out, int64_t ldo,
                             int flags, void* ws, size_t ws_bytes, qlin_stream_t stream) {
     QLIN_CHECK(check_attn(cache, B, max_q, Hq));
-    if (flags != 0 || window < 0 || !isfinite(scale)) return QLIN_ERR_INVALID_ARG;
+    if (flags != 0 || window < 0 || !isfinite(scale * cache->k_scale * 2.0f)) return QLIN_ERR_INVALID_ARG;
     if (total_q < 0 || total_q > kMaxTokens || max_pages < 1 || ldb < max_pages || ldb >= kMaxLd)
         return QLIN_ERR_INVALID_ARG;
-    if (max_pages > (((int64_t)1 << 30) / cache->page)) return QLIN_ERR_INVALID_ARG;
+    if (max_pages > kMaxContext / cache->page) return QLIN_ERR_INVALID_ARG;
     if (total_q == 0) return QLIN_OK;
     if (!block_table || !seq_lens || !cu_q) return QLIN_ERR_INVALID_ARG;
     QLIN_CHECK(check_rows(q, QLIN_BF16, ldq, (int64_t)Hq * cache->D));

@@ -37,7 +37,9 @@ constexpr int kSoftRegs = 152, kDqRegs = 112, kMmaRegs = 96;
 static_assert(kDqRegs < 128 && kMmaRegs < 128 && 256 * kSoftRegs + 128 * kDqRegs + 128 * kMmaRegs <= 512 * 128,
               "the launch's registers");
 constexpr int kMaxSeqs = 1024;
-constexpr int kItems = 4;      // descriptions in the ring
+// Descriptions in the ring.  The dequantizing warps take up to two tiles' pieces beyond the one that the softmax warps work
+// on, and the empty ones between them, which is no more than the last round's two parts and the end mark: five in all.
+constexpr int kItems = 8;
 // What a unit costs beside its tiles, and what joining its parts does, in tiles (2.4 us): queries in and rows out; the parts'
 // way through the workspace; reading one (131 KB at what an SM gets).
 constexpr float kUnitCost = 2.f, kJoinCost = 1.5f, kPartCost = 0.3f;
@@ -125,6 +127,7 @@ __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.
 struct Item {
     int b, h, base, rows, n, L, t0, t1;
     int64_t row0;
+    int first;        // the first place that its first row sees
     int part, parts;  // part of a unit that several CTAs share (parts > 1)
     int tail;         // its number among the shared ones
 };
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             const int r = it.base + srow;
             const int64_t slot = it.parts > 1 ? (int64_t)(it.tail * it.parts + it.part) : 0;
             float* part = a.parts + slot * kRows * (D + 2);  // [D / 4][256 rows] of four values, then [256] {m, l}
-            const float inv = l > 0.f ? a.cache.v_scale / l : 0.f;
+            const float inv = l == 0.f ? 0.f : a.cache.v_scale / l;
             __nv_bfloat16* dst = a.out + (it.row0 + group_div(a, r)) * a.ldo + (int64_t)(it.h * a.G + group_mod(a, r)) * D;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                         factor[s * kRows] = f;
                         lj += ml.y * f;
                     }
-                    const float invj = lj > 0.f ? a.cache.v_scale / lj : 0.f;
+                    const float invj = lj == 0.f ? 0.f : a.cache.v_scale / lj;
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
                         float4 acc[4] = {};
@@ -542,7 +545,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
         int tile = more ? ring[k % kItems].t0 - 1 : 0;
         auto group = [&](int tok, bool& bad_page) -> const uint8_t* {
             const Item& it = ring[k % kItems];
-            if (tok >= it.L) return nullptr;
+            if (tok >= it.L || (tok | (kGroup - 1)) < it.first) return nullptr;
             const int page = __ldg(a.table + it.b * a.ldb + (tok >> a.cache.page_log));
             if (page < 0 || page >= a.cache.n_pages) {
                 atomicOr(a.status, kStatusBad);
@@ -738,13 +741,16 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                 it.row0 = row0[lo];
                 it.rows = min(*unit_rows, it.n * a.G - it.base);
                 const int p0 = it.L - it.n + group_div(a, it.base), p1 = it.L - it.n + group_div(a, it.base + it.rows - 1);
-                const int first = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
-                it.t0 = first / kTok;
+                it.first = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
+                it.t0 = it.first / kTok;
                 it.t1 = p1 < 0 ? it.t0 : p1 / kTok + 1;
                 it.part = 0, it.parts = 1, it.tail = -1;
                 return it;
             };
-            const int units = prefix[a.B] * a.cache.Hkv;
+            // rows that sequences share (cu_q not rising) could number more units than an int holds
+            const int64_t all_units = (int64_t)prefix[a.B] * a.cache.Hkv;
+            const int units = all_units < (1 << 30) ? (int)all_units : 0;
+            if (units != all_units && lane == 0) atomicOr(a.status, kStatusBad);
             const int grid = gridDim.x, whole = units / grid * grid, tails = units - whole;
             // splits of the last round's units: their rounds times a part's tiles and its fixed cost, the least of it
             int splits = 1;
@@ -763,8 +769,8 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                 }
             }
             const int items = whole + tails * splits;
-            bool more = true;
-            for (int k = 0; more; ++k) {
+            int pushed = 0;
+            for (int k = 0;; ++k) {
                 // rounds go there and back
                 const int i = k * grid + ((k & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
                 Item it = {};
@@ -774,15 +780,26 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                 } else if (i < items) {
                     const int r = (i - whole) / splits, s = (i - whole) % splits;
                     it = unit(whole + r);
-                    const int cnt = it.t1 - it.t0, first = it.t0;
-                    it.t0 = first + (int)((int64_t)cnt * s / splits);
-                    it.t1 = first + (int)((int64_t)cnt * (s + 1) / splits);
                     it.part = s, it.parts = splits, it.tail = r;
                 }
-                more = it.b >= 0;  // only the last round has places without work
-                if (k >= kItems && !warp_wait(&itemfree[k % kItems], (k / kItems - 1) & 1)) break;
-                if (lane == 0) ring[k % kItems] = it;
-                warp_arrive(&itemfull[k % kItems]);
+                if (it.b >= 0 && it.t0 >= it.t1) {  // a unit that sees nothing: rows of zeros, no work for the others
+                    for (int j = lane; it.part == 0 && j < it.rows * (D / 8); j += 32) {
+                        const int row = it.base + j / (D / 8);
+                        *(reinterpret_cast<uint4*>(a.out + (it.row0 + group_div(a, row)) * a.ldo +
+                                                   (int64_t)(it.h * a.G + group_mod(a, row)) * D) + j % (D / 8)) = make_uint4(0, 0, 0, 0);
+                    }
+                    continue;
+                }
+                if (it.parts > 1) {
+                    const int cnt = it.t1 - it.t0, first = it.t0;
+                    it.t0 = first + (int)((int64_t)cnt * it.part / splits);
+                    it.t1 = first + (int)((int64_t)cnt * (it.part + 1) / splits);
+                }
+                if (pushed >= kItems && !warp_wait(&itemfree[pushed % kItems], (pushed / kItems - 1) & 1)) break;
+                if (lane == 0) ring[pushed % kItems] = it;
+                warp_arrive(&itemfull[pushed % kItems]);
+                ++pushed;
+                if (it.b < 0) break;  // only the last round has places without work
             }
         }
     }

@@ -33,11 +33,15 @@ __device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
 
 constexpr int kMaxParts = 512;  // CTAs of a launch at most: tickets in the workspace
 
-// The tile of the first place that the first of a sequence's n queries sees.
+// The first place that the first of a sequence's n queries sees, and its tile.  Groups of the cache that lie before it are
+// not looked at, nor their pages' numbers: a user may have given the pages away.
+__device__ __forceinline__ int first_seen(const AttnArgs& a, int n, int L) {
+    const int lo = a.window > 0 ? L - n + 1 - a.window : 0;
+    return lo > 0 ? lo : 0;
+}
 template <int TILE>
 __device__ __forceinline__ int first_tile(const AttnArgs& a, int n, int L) {
-    const int lo = a.window > 0 ? L - n + 1 - a.window : 0;
-    return lo > 0 ? lo / TILE : 0;
+    return first_seen(a, n, L) / TILE;
 }
 // A sequence's queries and context; bad ones are skipped.
 struct Seq {

@@ -177,11 +177,11 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         const int s = istage, e = issued % C::kBatch;
         if (e == 0) {
             // where the next kBatch tiles lie, a group a lane: the searches and the page table's latency once for all
-            uint32_t src = 0xffffffffu;  // behind the end, or a bad page: not copied, and masked
+            uint32_t src = 0xffffffffu;  // not seen, or a bad page: not copied, and masked
             if (issued + lane / NG < mine) {
                 const Cursor c = locate(t0 + warp + (int64_t)(issued + lane / NG) * W);
                 const int tok = (first_tile<TILE>(a, queries(c.b), length[c.b]) + c.i) * TILE + (lane % NG) * kGroup;
-                if (tok < length[c.b]) {
+                if (tok < length[c.b] && tok + kGroup > first_seen(a, queries(c.b), length[c.b])) {
                     const int page = __ldg(a.table + c.b * a.ldb + (tok >> a.cache.page_log));
                     if (page >= 0 && page < a.cache.n_pages)
                         src = (unsigned)page * heads_groups + ((unsigned)(c.hr / a.RB) << (a.cache.page_log - 4)) +
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                     sum += f * ml.y;
                 }
                 if (whole) {
-                    const float inv = sum > 0.f ? a.cache.v_scale / sum : 0.f;
+                    const float inv = sum == 0.f ? 0.f : a.cache.v_scale / sum;
                     const int rr = rb * C::kRows + nt * 8 + r;
                     *reinterpret_cast<__nv_bfloat162*>(a.out + (qrow + group_div(a, rr)) * a.ldo +
                                                        (int64_t)(h * a.G + group_mod(a, rr)) * D + 2 * pair) =
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                         __syncthreads();
                     }
                     if (sp == 0 && r < rows) {
-                        const float inv = sum > 0.f ? a.cache.v_scale / sum : 0.f;
+                        const float inv = sum == 0.f ? 0.f : a.cache.v_scale / sum;
                         const int rr = rb * C::kRows + r;
                         __nv_bfloat16* dst = a.out + (qrow + group_div(a, rr)) * a.ldo + (int64_t)(h * a.G + group_mod(a, rr)) * D + lane * V;
 #pragma unroll

@@ -4,9 +4,12 @@
 // Per head: n = h * w / sqrt(mean(h^2) + eps), then the first rot values in pairs (a, b) ->
 // (a c - b s, b c + a s).  Bound by memory: every value is read and written once.  A lane holds two runs of 4 values of a
 // head, D / 8 lanes a head: in the half-split rotation values i .. i + 3 and i + rot / 2 .., so that it has both members
-// of its pairs and needs no other lane; elsewhere 8 neighbours.  A warp works on one token and on 8 heads of one kind
-// (queries, keys, values): their loads are all in flight before the token's row of cosines and sines, which needs its
-// position, is asked for.
+// of its pairs and needs no other lane; elsewhere 8 neighbours.  (Where keys are quantized and an odd multiple of 16
+// values is rotated: 8 neighbours and a shuffle, for a block of 16 values would be torn between the runs.)  A warp
+// works on one token and on some heads of one kind (queries, keys, values): their loads are all in flight before the
+// token's row of cosines and sines, which needs its position, is asked for.
+#include <cuda/std/type_traits>
+
 #include "kv_cache.cuh"
 
 namespace qlin {
@@ -33,6 +36,8 @@ struct RopeArgs {
     Cache cache;
     unsigned* status;
 };
+
+enum Turn { kInterleaved, kSplit, kShuffled };  // how a lane meets the other members of its pairs
 
 // A lane's two runs of 4 values as they lie in memory, and as fp32.
 template <typename X>
@@ -83,20 +88,25 @@ __device__ __forceinline__ void store8(Y* p, const float (&v)[8]) {
     store4(p + 4, v + 4);
 }
 
-// The cosines and sines of a lane's four pairs.
-template <bool INTER>
-__device__ __forceinline__ void load_turn(const float* row, int rot, int d0, float (&c)[4], float (&s)[4]) {
-    const int i = INTER ? d0 / 2 : d0;
+// The cosines and sines of a lane's four (eight) pairs.
+template <int TURN>
+__device__ __forceinline__ void load_turn(const float* row, int rot, int d0, float (&c)[8], float (&s)[8]) {
+    const int i = TURN == kInterleaved ? d0 / 2 : TURN == kSplit || d0 < rot / 2 ? d0 : d0 - rot / 2;
     const float4 a = *reinterpret_cast<const float4*>(row + i), b = *reinterpret_cast<const float4*>(row + rot / 2 + i);
     c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
     s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
+    if constexpr (TURN == kShuffled) {  // eight pairs, with one member each here
+        const float4 e = *reinterpret_cast<const float4*>(row + i + 4), f = *reinterpret_cast<const float4*>(row + rot / 2 + i + 4);
+        c[4] = e.x, c[5] = e.y, c[6] = e.z, c[7] = e.w;
+        s[4] = f.x, s[5] = f.y, s[6] = f.z, s[7] = f.w;
+    }
 }
 
 // Norm (where `norm` says so) and rotation (of the lanes that `turn`) of one head in the arithmetic of R: float, or
 // double for keys that are quantized.  Every lane of the D / 8 lanes of a head calls it.
-template <typename R, int D, bool INTER>
-__device__ __forceinline__ void norm_rope(float (&v)[8], bool norm, const float (&w)[8], float eps, bool turn,
-                                          const float (&c)[4], const float (&s)[4]) {
+template <typename R, int D, int TURN>
+__device__ __forceinline__ void norm_rope(float (&v)[8], bool norm, const float (&w)[8], float eps, bool turn, int rot, int d0,
+                                          const float (&c)[8], const float (&s)[8]) {
     R n[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) n[j] = (R)v[j];
@@ -115,10 +125,19 @@ __device__ __forceinline__ void norm_rope(float (&v)[8], bool norm, const float 
 #pragma unroll
         for (int j = 0; j < 8; ++j) n[j] = n[j] * r * (R)w[j];
     }
-    if (turn) {
+    if constexpr (TURN == kShuffled) {
+        const int lane = threadIdx.x & 31;
+        const bool lo = d0 < rot / 2;
+        const int other = !turn ? lane : lo ? lane + rot / 16 : lane - rot / 16;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const R o = __shfl_sync(0xffffffffu, n[j], other);
+            if (turn) n[j] = lo ? n[j] * (R)c[j] - o * (R)s[j] : n[j] * (R)c[j] + o * (R)s[j];
+        }
+    } else if (turn) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            R &a = n[INTER ? 2 * j : j], &b = n[INTER ? 2 * j + 1 : j + 4];
+            R &a = n[TURN == kInterleaved ? 2 * j : j], &b = n[TURN == kInterleaved ? 2 * j + 1 : j + 4];
             const R x = a, y = b;
             a = x * (R)c[j] - y * (R)s[j];
             b = y * (R)c[j] + x * (R)s[j];
@@ -159,7 +178,7 @@ __device__ __forceinline__ float amax4(const float* v) {
 }
 
 // APPEND: heads are [q | k | v]; q to bf16 rows, k and v to the cache.  Otherwise [q | k] to rows of Y.
-template <typename X, typename Y, int D, bool INTER, bool APPEND>
+template <typename X, typename Y, int D, int TURN, bool APPEND>
 __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs a) {
     constexpr int LPH = D / 8, HPW = 32 / LPH;         // lanes a head, heads a warp at once
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -175,7 +194,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs
     const int heads = kind == 0 ? a.Hq : a.Hkv, base = kind == 0 ? 0 : kind == 1 ? a.Hq : a.Hq + a.Hkv;
     const int sub = lane / LPH, l = lane % LPH;
     const bool turn = kind < 2 && l < a.rot / 8;  // this lane's values are rotated
-    const bool split = !INTER && turn;            // its two runs lie half the rotated part apart
+    const bool split = TURN == kSplit && turn;            // its two runs lie half the rotated part apart
     const int d0 = split ? 4 * l : 8 * l, d1 = split ? a.rot / 2 + 4 * l : 8 * l + 4;
     const int h0 = c * (kind == 0 ? kHeadsPerWarp : KVH) + sub;  // heads h0, h0 + HPW, ..
     const X* row = reinterpret_cast<const X*>(a.x) + t * a.ldx + (int64_t)base * D;
@@ -193,7 +212,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs
     const int64_t pos = a.rot > 0 ? a.pos[t] : 0;
     const float* wp = kind == 0 ? a.qw : a.kw;
     const bool norm = kind < 2 && wp != nullptr;
-    float cs[4], sn[4], w[8];
+    float cs[8], sn[8], w[8];
     if (norm) {
         Raw8<float> rw;
         rw.load(wp, d0, d1);
@@ -208,14 +227,14 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs
         if (lane == 0) atomicOr(a.status, kStatusBad);
         return;
     }
-    if (turn) load_turn<INTER>(a.cs + pos * a.rot, a.rot, d0, cs, sn);
+    if (turn) load_turn<TURN>(a.cs + pos * a.rot, a.rot, d0, cs, sn);
     if (!APPEND || kind == 0) {
         Y* out = kind == 0 ? reinterpret_cast<Y*>(a.q) + t * a.ldq : reinterpret_cast<Y*>(a.k) + t * a.ldk;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float v[8];
             raw[i].get(v);
-            norm_rope<float, D, INTER>(v, norm, w, a.eps, turn, cs, sn);
+            norm_rope<float, D, TURN>(v, norm, w, a.eps, turn, a.rot, d0, cs, sn);
             if (h0 + i * HPW < heads) {
                 Y* dst = out + (int64_t)(h0 + i * HPW) * D;
                 store4(dst + d0, v);
@@ -232,7 +251,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs
         for (int i = 0; i < NKV; ++i) {
             float v[8];
             raw[i].get(v);
-            if (!isv) norm_rope<double, D, INTER>(v, norm, w, a.eps, turn, cs, sn);
+            if (!isv) norm_rope<double, D, TURN>(v, norm, w, a.eps, turn, a.rot, d0, cs, sn);
             // a block of 16 values: both runs of two lanes, or one run of four (the same branch for all lanes but where a
             // head is rotated in part)
             float m0 = amax4(v), m1 = amax4(v + 4);
@@ -311,12 +330,19 @@ template <typename X, typename Y, bool APPEND>
 static cudaError_t launch_rope(const kv::RopeArgs& a, int D, bool inter, cudaStream_t s) {
     const int64_t blocks = (a.T * a.chunks + kv::kRopeWarps - 1) / kv::kRopeWarps;
     const dim3 grid((unsigned)blocks), block(kv::kRopeWarps * 32);
+    const auto with = [&](auto d) {
+        constexpr int DD = decltype(d)::value;
+        if (inter)
+            kv::qk_rope_kernel<X, Y, DD, kv::kInterleaved, APPEND><<<grid, block, 0, s>>>(a);
+        else if (!APPEND || a.rot % 32 == 0)
+            kv::qk_rope_kernel<X, Y, DD, kv::kSplit, APPEND><<<grid, block, 0, s>>>(a);
+        else if constexpr (APPEND)
+            kv::qk_rope_kernel<X, Y, DD, kv::kShuffled, APPEND><<<grid, block, 0, s>>>(a);
+    };
     if (D == 128)
-        inter ? kv::qk_rope_kernel<X, Y, 128, true, APPEND><<<grid, block, 0, s>>>(a)
-              : kv::qk_rope_kernel<X, Y, 128, false, APPEND><<<grid, block, 0, s>>>(a);
+        with(cuda::std::integral_constant<int, 128>());
     else
-        inter ? kv::qk_rope_kernel<X, Y, 64, true, APPEND><<<grid, block, 0, s>>>(a)
-              : kv::qk_rope_kernel<X, Y, 64, false, APPEND><<<grid, block, 0, s>>>(a);
+        with(cuda::std::integral_constant<int, 64>());
     return cudaGetLastError();
 }
 

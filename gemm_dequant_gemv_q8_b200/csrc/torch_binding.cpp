@@ -128,14 +128,13 @@ Scratch scratch(PyObject* o, int dev) {
     if (!t.is_cuda() || t.get_device() != dev || !t.is_contiguous()) fail(PyExc_TypeError, "%s must be contiguous and on the call's CUDA device", "ws");
     return {t.data_ptr(), t.nbytes()};
 }
-// The stream of the call: the device's current one, or the given handle.
+// The call's device, made current (the library works on the current one), and its current stream.
 struct Where {
-    c10::cuda::OptionalCUDAGuard guard;  // the library works on the current device
+    c10::cuda::OptionalCUDAGuard guard;
     qlin_stream_t stream;
-    Where(int dev, PyObject* handle) {
+    explicit Where(int dev) {
         if (c10::cuda::current_device() != dev) guard.set_index((c10::DeviceIndex)dev);
-        stream = handle == Py_None ? (qlin_stream_t)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream()
-                                   : (qlin_stream_t)(uintptr_t)integer(handle);
+        stream = (qlin_stream_t)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
     }
 };
 // cos_sin, q_weight, k_weight, eps, rot, flags
@@ -190,8 +189,8 @@ struct Held {  // drops its reference if the call fails
     }                                                                                  \
     PyObject* name##_(PyObject* const* a)
 
-// x, Hq, Hkv, D, positions, (cos_sin, q_weight, k_weight, eps, rot, flags), q, k, ydt, ws, stream
-CALL(qk_norm_rope, 16) {
+// x, Hq, Hkv, D, positions, (cos_sin, q_weight, k_weight, eps, rot, flags), q, k, ydt, ws
+CALL(qk_norm_rope, 15) {
     const int Hq = small(a[1]), Hkv = small(a[2]), D = small(a[3]), ydt = small(a[13]);
     const Input x = projections(a[0], (int64_t)(Hq + Hkv) * D, false);
     const qlin_qk_params p = params(a + 5, D, x.dev);
@@ -201,14 +200,14 @@ CALL(qk_norm_rope, 16) {
     const Rows k = rows(a[12], "k", dtype_of(ydt), *x.t, x.T, Hkv, D);
     Held hk{k.obj};
     const Scratch ws = scratch(a[14], x.dev);
-    const Where w(x.dev, a[15]);
+    const Where w(x.dev);
     check_status("qlin_qk_norm_rope", f_qk_norm_rope(x.t->data_ptr(), x.dt, x.T, x.ld, Hq, Hkv, D, &p, pos, q.p, q.ld, k.p, k.ld,
                                                      (qlin_dtype_t)ydt, 0, ws.p, ws.n, w.stream));
     return pair(hq.release(), hk.release());
 }
 
-// cache, device, x, Hq, Hkv, D, positions, slots, (cos_sin, q_weight, k_weight, eps, rot, flags), q, ws, stream
-CALL(kv_append, 17) {
+// cache, device, x, Hq, Hkv, D, positions, slots, (cos_sin, q_weight, k_weight, eps, rot, flags), q, ws
+CALL(kv_append, 16) {
     const qlin_kv_cache* c = cache_of(a[0]);
     const int dev = small(a[1]), Hq = small(a[3]), Hkv = small(a[4]), D = small(a[5]);
     const Input x = projections(a[2], (int64_t)(Hq + 2 * Hkv) * D, true);
@@ -219,14 +218,14 @@ CALL(kv_append, 17) {
     const Rows q = rows(a[14], "q", at::kBFloat16, *x.t, x.T, Hq, D);
     Held hq{q.obj};
     const Scratch ws = scratch(a[15], dev);
-    const Where w(dev, a[16]);
+    const Where w(dev);
     check_status("qlin_kv_append", f_kv_append(c, x.t->data_ptr(), x.dt, x.T, x.ld, Hq, &p, pos, slots, Hq ? q.p : nullptr, q.ld, 0,
                                                ws.p, ws.n, w.stream));
     return hq.release();
 }
 
-// cache, device, slots, Hkv, D, k, v, ydt, ws, stream
-CALL(kv_gather, 10) {
+// cache, device, slots, Hkv, D, k, v, ydt, ws
+CALL(kv_gather, 9) {
     const qlin_kv_cache* c = cache_of(a[0]);
     const int dev = small(a[1]), Hkv = small(a[3]), D = small(a[4]), ydt = small(a[7]);
     const at::Tensor& s = on_device(a[2], "slots", at::kInt, dev);
@@ -238,13 +237,13 @@ CALL(kv_gather, 10) {
     Held hv{v.obj};
     if (k.ld != (int64_t)Hkv * D || v.ld != (int64_t)Hkv * D) fail(PyExc_ValueError, "%s must be contiguous", "k and v");
     const Scratch ws = scratch(a[8], dev);
-    const Where w(dev, a[9]);
+    const Where w(dev);
     check_status("qlin_kv_gather", f_kv_gather(c, T, slots, k.p, v.p, (qlin_dtype_t)ydt, ws.p, ws.n, w.stream));
     return pair(hk.release(), hv.release());
 }
 
-// cache, device, D, q, block_table, seq_lens, cu_q, max_q, scale, window, out, ws, stream
-CALL(attn_kv4, 13) {
+// cache, device, D, q, block_table, seq_lens, cu_q, max_q, scale, window, out, ws
+CALL(attn_kv4, 12) {
     const qlin_kv_cache* c = cache_of(a[0]);
     const int dev = small(a[1]), D = small(a[2]), max_q = small(a[7]), window = small(a[9]);
     const at::Tensor& qt = on_device(a[3], "q", at::kBFloat16, dev);
@@ -263,7 +262,7 @@ CALL(attn_kv4, 13) {
     const Rows out = rows(a[10], "out", at::kBFloat16, qt, total, Hq, D);
     Held ho{out.obj};
     const Scratch ws = scratch(a[11], dev);
-    const Where w(dev, a[12]);
+    const Where w(dev);
     check_status("qlin_attn_kv4",
                  f_attn_kv4(c, q.p, q.ld, static_cast<const int32_t*>(table.data_ptr()), B > 1 ? table.stride(0) : table.size(1),
                             (int)table.size(1), plens, cu, (int)B, max_q, total, (int)Hq, real(a[8]), window, out.p, out.ld, 0,

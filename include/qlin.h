@@ -436,7 +436,8 @@ typedef struct qlin_qk_params {
  *       ldx elements, 16-byte aligned rows (ldx a multiple of 4 (fp32) or 8 (bf16))
  *   positions : T int32, the tokens' rows of cos_sin; not read where rot is 0
  *   q, k : T rows of Hq * D and Hkv * D values, fp32 or bf16 (ydt), row strides ldq and ldk elements,
- *       rows aligned as x's; the arithmetic is fp32, rounded once.  q and k may overwrite x's
+ *       rows aligned as x's; the arithmetic is fp32 (squares of values above 2^63 overflow, and their
+ *       head becomes 0), rounded once.  q and k may overwrite x's
  *       own heads (q = x, k = x + Hq * D, the same strides and type), and nothing else of x.
  *   ws : 256 bytes (the status word), zero-filled before first use
  * T = 0 does nothing.  A position outside [0, n_pos) leaves its token's q and k rows unwritten and
@@ -482,12 +483,16 @@ size_t qlin_attn_kv4_workspace_bytes(const qlin_kv_cache* cache, int B, int max_
  * that sees nothing (p < 0) gives a row of zeros.  Single tokens (n = 1) and prompt chunks are the same
  * call.  What the cache holds behind a sequence's end is never used, whatever its bits.
  *   q, out : total_q rows of Hq * D bf16, row strides ldq and ldo elements, 16-byte aligned rows; rows
- *       outside cu_q[0] .. cu_q[B] are left as they are.  The products are exact values of K and V
- *       with q and with probabilities in fp16; scores, softmax sums and outputs are fp32, rounded once.
- *   block_table : B rows of int32 page numbers, row stride ldb, max_pages columns: token t of sequence b
- *       is token t % page of page block_table[b * ldb + t / page]
- *   seq_lens : B int32; cu_q : B + 1 int32; both device arrays, so one captured graph serves any lengths
- *   max_q : the most queries of one sequence in this call (it sizes the grid); Hq a multiple of Hkv,
+ *       outside cu_q[0] .. cu_q[B] are left as they are; out is no part of q.  The products are exact
+ *       values of K and V with q and with probabilities in fp16; scores, softmax sums and outputs are
+ *       fp32, rounded once.  Scores have to stay finite in fp32, or their row is NaN
+ *   block_table : B rows of int32 page numbers, row stride ldb, max_pages columns (max_pages * page <=
+ *       2^26): token t of sequence b is token t % page of page block_table[b * ldb + t / page].  Sequences
+ *       may share pages.  Numbers of pages with no token that a query of the sequence sees (behind its
+ *       context, before the window) are not looked at
+ *   seq_lens : B int32; cu_q : B + 1 int32, not falling; both device arrays, so one captured graph serves any lengths
+ *   scale : finite, and 2 * scale * k_scale too
+ *   max_q : the most queries of one sequence in this call (it chooses the kernel and sizes ws); Hq a multiple of Hkv,
  *       Hq / Hkv <= 64; B <= 1024
  *   ws : qlin_attn_kv4_workspace_bytes(cache, B, max_q, Hq) bytes, zero-filled before first use; it may
  *       be reused by any later qlin_attn_kv4 call on the same stream for which it is large enough

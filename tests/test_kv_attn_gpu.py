@@ -97,6 +97,10 @@ APPEND = [  # T, Hq, Hkv, D, rot, interleaved, norm, x, page, ks, vs
     (45, 4, 4, 128, 64, True, False, BF16, 64, 0.01, 0.3),
     (130, 3, 1, 64, 64, False, True, BF16, 128, 3.0, 1.0),
     (77, 16, 8, 128, 0, False, True, F32, 256, 1.0, 0.125),
+    (33, 4, 2, 64, 48, False, True, F32, 16, 1.0, 1.0),    # an odd number of blocks rotated, by halves
+    (21, 2, 3, 128, 16, False, True, BF16, 32, 0.7, 1.0),
+    (9, 1, 5, 128, 112, False, False, F32, 16, 1.0, 1.0),
+    (12, 2, 2, 128, 48, True, True, F32, 16, 1.0, 1.0),
 ]
 
 
@@ -466,6 +470,208 @@ def test_attention_cache_beyond_32_bits(nq):
     gk, _ = q.qlin_kv_gather(kv, last, ydt=q.QLIN_F32)
     kc, kb = ref.quantize(x[:, :Hkv * D].view(1, Hkv, D), 1.0)
     assert torch.equal(gk.cpu(), ref.values(kc, kb).float())
+
+
+@pytest.mark.parametrize("B,nq,Hq,Hkv", [(300, 1, 4, 2), (1024, 1, 2, 2), (1024, 3, 16, 1)])
+def test_attention_many_sequences(B, nq, Hq, Hkv):
+    # more sequences than one launch takes; empty ones among them
+    D, page = 64, 16
+    lens = [(37 * b) % 71 for b in range(B)]
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, [nq] * B, Hq, Hkv, D, page, 85)
+    o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs)
+    assert st == 0
+    check_attn(o, ln, cu, qs, ks, vs, D, D ** -0.5)
+
+
+@pytest.mark.parametrize("nq", [1, 5, 70])
+@pytest.mark.parametrize("window", [1, 40, 300])
+def test_attention_pages_before_the_window_are_free(nq, window):
+    # a user may give the pages before the window away: numbers outside the cache, or any bits in them
+    lens, Hq, Hkv, D, page = [700, 333, 128], 8, 2, 128, 16
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, [nq] * 3, Hq, Hkv, D, page, 86)
+    pages = c.view(-1, q.qlin_kv_cache_bytes(1, page, Hkv, D))
+    for b, L in enumerate(lens):
+        gone = max(0, L - nq - window + 1) // page  # whole pages that no query sees
+        for j in range(gone):
+            pages[table[b, j]] = 0x7F
+            if b != 1:
+                table[b, j] = -1
+    o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs, window=window)
+    assert st == 0
+    check_attn(o, ln, cu, qs, ks, vs, D, D ** -0.5, window)
+
+
+@pytest.mark.parametrize("nq", [1, 33])
+def test_attention_shared_pages(nq):
+    # sequences with a common beginning, one of them twice, and one whose page table repeats a page
+    Hq, Hkv, D, page = 8, 2, 64, 32
+    c, k, v = ref.random_cache(12, page, Hkv, D, gen(87))
+    rows = [[0, 1, 2, 3, 4], [0, 1, 2, 5, 6], [0, 1, 2, 3, 4], [7, 7, 7, 0, 7]]
+    lens = [150, 139, 150, 160]
+    table, ln = torch.tensor(rows, dtype=torch.int32), torch.tensor(lens, dtype=torch.int32)
+    cu = torch.arange(5, dtype=torch.int32) * nq
+    qs = [torch.randn(nq, Hq, D, generator=gen(88 + b % 2)).bfloat16() for b in range(4)]
+    o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs)
+    assert st == 0
+    idx = [(torch.tensor(r)[:, None] * page + torch.arange(page)).flatten()[:L] for r, L in zip(rows, lens)]
+    check_attn(o, ln, cu, qs, [k[i] for i in idx], [v[i] for i in idx], D, D ** -0.5)
+    assert torch.equal(o[:nq], o[2 * nq:3 * nq])
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, 1e-30])
+@pytest.mark.parametrize("nq", [1, 70])
+def test_attention_any_scale(nq, scale):
+    lens, Hq, Hkv, D, page = [200, 31], 4, 2, 64, 16
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, [nq, min(nq, 31)], Hq, Hkv, D, page, 90)
+    o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs, scale=scale)
+    assert st == 0
+    check_attn(o, ln, cu, qs, ks, vs, D, scale)
+
+
+@pytest.mark.parametrize("nq", [1, 5, 70])
+def test_attention_rows_of_nan_and_infinity_stay_alone(nq):
+    lens, Hq, Hkv, D, page = [300], 8, 1, 128, 16
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, [nq], Hq, Hkv, D, page, 91)
+    bad = [t.clone() for t in qs]
+    bad[0][:, 1, 3] = float("nan")
+    bad[0][:, 4, 7] = float("inf")
+    bad[0][:, 6] = -float("inf")
+    o, _ = run_attn(c, page, Hkv, D, table, ln, cu, bad)
+    clean, _ = run_attn(c, page, Hkv, D, table, ln, cu, qs)
+    keep = [0, 2, 3, 5, 7]
+    check_attn(clean, ln, cu, qs, ks, vs, D, D ** -0.5)
+    assert torch.isnan(o[:, 1]).all()
+    out, tp, ts, tv = ref.attention(qs[0].double(), ks[0], vs[0], 300, D ** -0.5)
+    err = (o.cpu().double() - out).abs() <= ref.attention_tol(out, tp, ts, tv, D, 300)
+    assert err[:, keep].all()
+
+
+def test_attention_falling_rows_are_refused_by_the_status():
+    lens, Hq, Hkv, D, page = [90, 60, 33], 4, 2, 64, 16
+    c, table, ln, _, qs, ks, vs = attn_case(lens, [4, 3, 2], Hq, Hkv, D, page, 92)
+    for nq_max in (4, 200):  # few rows, and the other kernel
+        cu = torch.tensor([4, 8, 2, 4], dtype=torch.int32)
+        rows = torch.cat([torch.zeros(2, Hq, D).bfloat16(), qs[2], qs[0]])
+        out = torch.full((8, Hq, D), 7.0, dtype=BF16, device="cuda")
+        o, st = run_attn(c, page, Hkv, D, table, ln, cu, [rows], max_q=nq_max, out=out)
+        assert st == 1 and (o[:2] == 7).all()
+        check_attn(o[4:], ln[:1], torch.tensor([0, 4]), qs[:1], ks[:1], vs[:1], D, D ** -0.5)
+        check_attn(o[2:4], ln[2:], torch.tensor([0, 2]), qs[2:], ks[2:], vs[2:], D, D ** -0.5)
+
+
+def test_attention_max_q_above_the_queries():
+    # the bound on the queries chooses the kernel: single tokens through each
+    lens, Hq, Hkv, D, page = [500, 64, 1, 0], 8, 2, 128, 16
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, [1] * 4, Hq, Hkv, D, page, 93)
+    for mq in (1, 2, 3, 8, 9, 32, 33, 4000):
+        o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs, max_q=mq)
+        assert st == 0
+        check_attn(o, ln, cu, qs, ks, vs, D, D ** -0.5)
+
+
+@pytest.mark.parametrize("rows", [32, 36, 128, 132])
+@pytest.mark.parametrize("B", [1, 9])
+def test_attention_on_both_sides_of_the_choice(rows, B):
+    Hq, Hkv, D, page = 8, 2, 64, 16
+    lens = [200 + 13 * b for b in range(B)]
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, [rows // 4] * B, Hq, Hkv, D, page, 94 + rows)
+    o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs)
+    assert st == 0
+    check_attn(o, ln, cu, qs, ks, vs, D, D ** -0.5)
+
+
+def test_attention_one_workspace_for_many_shapes_and_two_graphs():
+    # every call leaves the workspace fit for any other that it is large enough for; graphs that share it run in turn
+    Hq, Hkv, D, page = 8, 2, 128, 16
+    shapes = [([3000], 1), ([900, 30, 5], 70), ([2000, 700], 6), ([60, 1200], 1), ([1500], 257)]
+    cases = [attn_case(lens, [min(nq, L) for L in lens], Hq, Hkv, D, page, 95 + i) for i, (lens, nq) in enumerate(shapes)]
+    calls, need = [], 0
+    for (lens, nq), (c, table, ln, cu, qs, ks, vs) in zip(shapes, cases):
+        kv = q.KVCache(dev_cache(c), page, Hkv, D)
+        need = max(need, q.qlin_attn_kv4_workspace_bytes(kv, len(lens), nq, Hq))
+        calls.append((kv, torch.cat(qs).cuda(), table.cuda(), ln.cuda(), cu.cuda(), nq))
+    ws = q.workspace(need)
+    alone = [q.qlin_attn_kv4(*call) for call in calls]
+    for o, (c, table, ln, cu, qs, ks, vs) in zip(alone, cases):
+        check_attn(o, ln, cu, qs, ks, vs, D, D ** -0.5)
+    for i in (0, 1, 2, 3, 4, 3, 1, 4, 0, 2):
+        assert torch.equal(q.qlin_attn_kv4(*calls[i], ws=ws), alone[i]), i
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    for call in calls[:2]:
+        out = torch.empty_like(call[1])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            q.qlin_attn_kv4(*call, ws=ws, out=out)
+        graphs.append((graph, out))
+    for _ in range(3):
+        for (graph, out), want in zip(graphs, alone):
+            out.zero_()
+            graph.replay()
+            assert torch.equal(out, want)
+    assert q.qlin_ws_status(ws) == 0
+
+
+def test_calls_on_two_streams_at_once():
+    # append, read-back and attention of two caches side by side, each with a workspace of its own; the stream argument
+    Hq, Hkv, D, page, T = 8, 2, 128, 16, 700
+    x = [torch.randn(T, (Hq + 2 * Hkv) * D, generator=gen(i)).cuda() for i in (1, 2)]
+    pos, cs = torch.arange(T, dtype=torch.int32).cuda(), ref.table(T, D).cuda()
+    table = torch.arange(44, dtype=torch.int32)[None].cuda()
+    lens, cu = torch.tensor([T], dtype=torch.int32).cuda(), torch.tensor([0, T], dtype=torch.int32).cuda()
+    one = torch.tensor([0, 1], dtype=torch.int32).cuda()
+
+    def run(cache, x, ws, **kw):
+        qo = q.qlin_kv_append(cache, x, Hq, pos, pos, cs, ws=ws, **kw)
+        a = q.qlin_attn_kv4(cache, qo, table, lens, cu, T, ws=ws, **kw)
+        b = q.qlin_attn_kv4(cache, qo[-1:], table, lens, one, 1, ws=ws, **kw)
+        return [qo, a, b, *q.qlin_kv_gather(cache, pos, ws=ws, **kw)]
+
+    caches = [q.kv_cache(44, page, Hkv, D) for _ in x]
+    n = max(q.qlin_attn_kv4_workspace_bytes(caches[0], 1, m, Hq) for m in (1, T))
+    want = [run(c, xi, q.workspace(n)) for c, xi in zip(caches, x)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    fresh = [q.kv_cache(44, page, Hkv, D) for _ in x]
+    ws = [q.workspace(n) for _ in x]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        got = [run(c, xi, w, stream=s) for c, xi, w, s in zip(fresh, x, ws, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+    qk = q.qlin_qk_norm_rope(x[0], Hq, Hkv, D, pos, cs, stream=streams[0])
+    streams[0].synchronize()
+    assert torch.equal(qk[0], want[0][0])
+
+
+def test_calls_without_rows():
+    D, page = 64, 16
+    cache = q.kv_cache(2, page, 1, D)
+    before = cache.data.clone()
+    e = torch.zeros(0, dtype=torch.int32, device="cuda")
+    x = torch.zeros(0, 4 * D, device="cuda")
+    cs = ref.table(4, D).cuda()
+    qo, ko = q.qlin_qk_norm_rope(x, 2, 1, D, e, cs)
+    assert qo.shape == (0, 2, D) and ko.shape == (0, 1, D)
+    assert q.qlin_kv_append(cache, x, 2, e, e, cs).shape == (0, 2, D)
+    assert q.qlin_kv_gather(cache, e)[0].shape == (0, 1, D)
+    z = torch.zeros(2, dtype=torch.int32, device="cuda")
+    o = q.qlin_attn_kv4(cache, torch.zeros(0, 2, D, dtype=BF16, device="cuda"), z[None], z[:1], z, 1)
+    assert o.shape == (0, 2, D) and torch.equal(cache.data, before)
+
+
+def test_append_needs_no_positions_without_rotation_and_no_queries():
+    T, Hq, Hkv, D, page = 5, 3, 2, 64, 16
+    x = torch.randn(T, (Hq + 2 * Hkv) * D, generator=gen(12)).cuda()
+    slots = torch.arange(T, dtype=torch.int32).cuda()
+    w = torch.full((D,), 1.5).cuda()
+    a, b = q.kv_cache(1, page, Hkv, D), q.kv_cache(1, page, Hkv, D)
+    q.qlin_kv_append(a, x, Hq, None, slots, None, w, w)
+    q.qlin_kv_append(b, x[:, Hq * D:].contiguous(), 0, None, slots, None, None, w)
+    assert torch.equal(a.data, b.data)
 
 
 # ----------------------------------------------------------------------------- as they are used

@@ -110,7 +110,8 @@ def test_attention_refusals(lib):
                      (dict(out=0x600002), ALIGN), (dict(ldb=7), ARG), (dict(pages=0), ARG), (dict(pages=1 << 27, ldb=1 << 27), ARG),
                      (dict(B=0), ARG), (dict(B=1025), ARG), (dict(max_q=0), ARG), (dict(total=-1), ARG), (dict(Hq=3), ARG),
                      (dict(Hq=0), ARG), (dict(Hq=130, ldq=8320, ldo=8320), UNSUP), (dict(window=-1), ARG),
-                     (dict(scale=float("inf")), ARG), (dict(flags=1), ARG), (dict(ws=0), WS), (dict(n=8), WS),
+                     (dict(scale=float("inf")), ARG), (dict(scale=2e38), ARG), (dict(scale=1e30, c=cache(ks=1e10)), ARG),
+                     (dict(pages=(1 << 22) + 1, ldb=1 << 23), ARG), (dict(flags=1), ARG), (dict(ws=0), WS), (dict(n=8), WS),
                      (dict(ws=0x800080), ALIGN), (dict(table=0x500002), ALIGN)]:
         assert attn(lib, **kw) == want, kw
     assert attn(lib, total=0) == 0
