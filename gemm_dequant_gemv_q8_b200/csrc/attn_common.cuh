@@ -16,7 +16,7 @@ struct AttnArgs {
     float scale_log2;  // scale * k_scale * log2(e)
     int window;        // 0: none; below 2^30
     unsigned* status;
-    int RB, min_tiles;  // few rows: row blocks of a (sequence, head); fewest tiles that another CTA is worth
+    int RB;             // few rows: row blocks of a (sequence, head)
     int* tickets;       // in the workspace: kMaxParts, zero between calls
     float* parts;       // then the parts of what several CTAs share
 };

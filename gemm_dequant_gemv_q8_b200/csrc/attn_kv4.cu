@@ -12,8 +12,8 @@ namespace kv {
 
 // ------------------------------------------------------------------------------------- few rows, a long axis
 //
-// One persistent launch, one CTA an SM.  The work is a list of tiles (sequence, kv head, row block, 4608 bytes of
-// cache), cut into one equal contiguous range a CTA, so that a batch of any lengths keeps every SM busy to the end.
+// One persistent launch, one CTA an SM.  The work is a list of tiles (sequence, kv head, row block, 32 tokens), cut into
+// one equal contiguous range a CTA, so that a batch of any lengths keeps every SM busy to the end.
 // Within a CTA the tiles go round its warps; each warp has a ring of its own, filled by bulk copies of whole groups,
 // and a running maximum, sum and P V of its own.  Where a (sequence, head, row block) ends, the warps' parts are
 // joined in shared memory; where it is shared between CTAs, the last of them to finish joins their parts from the
@@ -24,6 +24,13 @@ namespace kv {
 // product of code and scale) whatever the group size.  The order of the inner axis is free as long as both
 // operands share it: for S it is the order in which a lane's 16 (8) bytes of a token's row hold the values, for P V the
 // lanes' tokens are four neighbours, whose codes of one block are 32 contiguous bytes.
+//
+// The cache has to be read once, and is; what bounds the kernel is the arithmetic that dequantizes it (one conversion a
+// byte and one product a pair of values: ALU pipe 50% busy, an instruction issued in 56% of the active cycles) beside
+// some 9 us of start and end (launch, lengths and pages, the joining).  64 sequences of up to 8192 tokens (8 kv heads of
+// 128, 374 MB): 102 us, 3.7 TB/s; the copies alone 67, without V's arithmetic 80, without K's 89.  1 x 131071 39 us
+// (3.9 TB/s); 16 x 4096 ragged (heads of 64, 24 MB) 20; 1 x 1000 9.5.  Warps: 16 give 102 / 41 / 20.1 us on the first
+// three (before the shares), 12 105 / 44 / 20.8, 8 114 / 47 / 21.1.
 template <int D, int NT>
 struct Dec {
     static constexpr int kWarps = NT == 1 ? 16 : 8;
@@ -41,6 +48,8 @@ struct Dec {
     static constexpr int smem(int B) { return kFixed + (3 * B + 2) * 4; }
 };
 constexpr int kMaxDecSeqs = 256;  // sequences of a launch
+// Fewest tiles that another CTA is worth (1 x 1000 tokens: 2 9.7 us, 4 9.3, 8 9.2, 16 10.4).
+constexpr int kMinTiles = 8;
 static_assert(Dec<128, 1>::smem(kMaxDecSeqs) <= 232448 && Dec<64, 1>::smem(kMaxDecSeqs) <= 232448 &&
                   Dec<128, 2>::smem(kMaxDecSeqs) <= 232448 && Dec<64, 2>::smem(kMaxDecSeqs) <= 232448,
               "shared memory");
@@ -81,6 +90,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
     uint8_t* qbuf = reinterpret_cast<uint8_t*>(source + W * 32);  // [2] this segment's queries and the next one's
     int* flag = reinterpret_cast<int*>(qbuf + 2 * C::kQBytes);
     int* longest = flag + 1;  // tiles of the longest sequence's segments
+    int *share = flag + 2, *place = flag + 3;  // tiles of a CTA's share, 0: equal parts; this CTA's sequence and its first CTA
     int* prefix = flag + 4;  // [B + 1] tiles of one (head, row block) before sequence b
     int *row0 = prefix + a.B + 1, *length = row0 + a.B + 1;  // [B + 1] first rows of q, [B] contexts
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -88,7 +98,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
 
     if (lane < S) mbar_init(&bars[warp * S + lane], NG);
     if (warp == 0) {
-        int run = 0, most = 0;
+        int run = 0, most = 0, some = 0;  // tiles, the most of a sequence, sequences with any
         for (int b0 = 0; b0 < a.B; b0 += 32) {
             const int b = b0 + lane;
             int v = 0;
@@ -99,6 +109,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                 if (s.bad && blockIdx.x == 0) atomicOr(a.status, kStatusBad);
             }
             most = max(most, v);
+            some += __popc(__ballot_sync(0xffffffffu, v > 0));
 #pragma unroll
             for (int k = 1; k < 32; k <<= 1) {
                 const int u = __shfl_up_sync(0xffffffffu, v, k);
@@ -109,6 +120,32 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         }
         most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) prefix[0] = 0, row0[0] = __ldg(a.cu), *longest = most;
+        // Equal parts of the list put two segments into most CTAs where these are few: a second joining.  There, whole
+        // numbers of CTAs for each segment, if shares of the equal parts' rounds of the warps (and one more where they are
+        // many) allow it (8 x 2048 16.7 -> 13.5 us, 1 x 131071 41.6 -> 39.4).  The search takes 0.9 us: not where
+        // it seldom finds such shares, nor for parts of less than a round (16 x 4096, 1 x 1000).
+        int tiles = 0, at = -1;
+        const int grid = gridDim.x;
+        if ((int64_t)some * HR * 2 <= grid && run * HR > grid * W) {
+            __syncwarp();
+            const int least = (run * HR + grid - 1) / grid, n = (least + W - 1) / W * W + (least > 4 * W ? W : 0);
+            int before = 0;
+            for (int b0 = 0; b0 < a.B; b0 += 32) {
+                const int b = b0 + lane, ctas = b < a.B ? (prefix[b + 1] - (b ? prefix[b] : 0) + n - 1) / n * HR : 0;
+                int v = ctas;
+#pragma unroll
+                for (int k = 1; k < 32; k <<= 1) {
+                    const int u = __shfl_up_sync(0xffffffffu, v, k);
+                    if (lane >= k) v += u;
+                }
+                const int first = before + v - ctas, me = blockIdx.x;
+                const unsigned here = __ballot_sync(0xffffffffu, me >= first && me < first + ctas);
+                if (here) at = __shfl_sync(0xffffffffu, b << 16 | first, __ffs(here) - 1);
+                before += __shfl_sync(0xffffffffu, v, 31);
+            }
+            if (before <= grid) tiles = n;
+        }
+        if (lane == 0) *share = tiles, *place = at;
     }
     fence_mbar_init();
     __syncthreads();
@@ -139,18 +176,24 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         c.i = (int)(u - (int64_t)c.hr * c.per);
         return c;
     };
-    // This CTA's range of tiles: the T-th parts of the list.  Where every segment is at most a tile a warp, the ranges
-    // end with segments: no parts to join between CTAs.
+    // This CTA's range of tiles: a share of one segment, or an equal part of the list.  Where every segment is at most a
+    // tile a warp, the parts end with segments: no parts to join between CTAs.
     const int64_t T = (int64_t)prefix[a.B] * HR;
     const bool whole_segs = *longest <= W;
-    const int64_t want = whole_segs ? (int64_t)a.B * HR : div_small(T + a.min_tiles - 1, a.min_tiles);
+    const int64_t want = whole_segs ? (int64_t)a.B * HR : div_small(T + kMinTiles - 1, kMinTiles);
     const int P = (int)(want < gridDim.x ? want : gridDim.x);
-    if ((int)blockIdx.x >= P || T == 0) return;
+    if (*share ? *place < 0 : (int)blockIdx.x >= P || T == 0) return;
     int64_t t0 = div_small(T * blockIdx.x, P), t1 = div_small(T * (blockIdx.x + 1), P);
     if (whole_segs) {
         t0 -= t0 < T ? locate(t0).i : 0;
         t1 -= t1 < T ? locate(t1).i : 0;
         if (t0 >= t1) return;
+    }
+    if (*share) {
+        const int b = *place >> 16, r = (int)blockIdx.x - (*place & 0xffff), per = prefix[b + 1] - prefix[b];
+        const int n = (per + *share - 1) / *share, hr = r / n, j = r - hr * n;
+        const int64_t start = (int64_t)prefix[b] * HR + (int64_t)hr * per;
+        t0 = start + div_small((int64_t)per * j, n), t1 = start + div_small((int64_t)per * (j + 1), n);
     }
 
     auto queries = [&](int b) { return row0[b + 1] - row0[b]; };
@@ -490,7 +533,13 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
             qnext = load_q(seg);
         }
         // join the warps' parts, 8 rows at a time, in the order of the warps
-        const int c0 = whole_segs ? 0 : (int)div_small((s0 + 1) * P - 1, T), c1 = whole_segs ? 0 : (int)div_small(s1 * P - 1, T);
+        int c0 = 0, c1 = 0;  // the CTAs that have tiles of the segment
+        if (*share) {
+            const int n = (seg.per + *share - 1) / *share;
+            c0 = (*place & 0xffff) + seg.hr * n, c1 = c0 + n - 1;
+        } else if (!whole_segs) {
+            c0 = (int)div_small((s0 + 1) * P - 1, T), c1 = (int)div_small(s1 * P - 1, T);
+        }
         const bool whole = c0 == c1;
         float* part = a.parts + (int64_t)(2 * blockIdx.x + ((int)blockIdx.x == c0)) * C::kRows * (D + 2);
 #pragma unroll
@@ -724,7 +773,6 @@ extern "C" cudaError_t qlin_launch_attn_kv4(const qlin_kv_cache* c, const void* 
     a.status = (unsigned*)ws;
     a.tickets = (int*)((uint8_t*)ws + 256);
     a.parts = (float*)((uint8_t*)ws + 256 + kv::kMaxParts * 4);
-    a.min_tiles = 8;
     const int64_t rows = (int64_t)max_q * a.G;
     if (!few_rows(rows, B, c->Hkv)) return qlin_launch_attn_chunk(&a, c->D, kv_sm_count(), s);
     a.RB = rows <= 8 ? 1 : (int)((rows + 15) / 16);

@@ -290,6 +290,26 @@ def test_decode(lens, Hq, Hkv, D, page, window):
     check_attn(o, ln, cu, qs, ks, vs, D, D ** -0.5, window)
 
 
+LONG = [  # lens, queries, Hq, Hkv, D, page, window
+    ([30000, 9000, 5, 0], 1, 32, 4, 128, 64, 0),    # whole CTAs for each segment
+    ([20000, 31, 7000], 4, 8, 2, 64, 16, 0),
+    ([30000, 9000], 1, 8, 8, 64, 256, 25000),
+    ([2080] * 18, 1, 8, 4, 64, 32, 0),              # equal parts: the shares would need more CTAs
+    ([6000 - 300 * b for b in range(9)], 1, 16, 8, 128, 16, 0),
+]
+
+
+@pytest.mark.parametrize("lens,nq,Hq,Hkv,D,page,window", LONG)
+def test_decode_long(lens, nq, Hq, Hkv, D, page, window):
+    nqs = [min(nq, L) if L else 1 for L in lens]
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, nqs, Hq, Hkv, D, page, 60 + len(lens))
+    o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs, window=window)
+    assert st == 0
+    check_attn(o, ln, cu, qs, ks, vs, D, D ** -0.5, window)
+    o2, _ = run_attn(c, page, Hkv, D, table, ln, cu, qs, window=window)
+    assert torch.equal(o, o2)
+
+
 CHUNK = [  # lens, queries, Hq, Hkv, D, page, window
     ([2], [2], 2, 1, 64, 16, 0),
     ([40, 9, 200], [4, 3, 1], 8, 2, 128, 16, 0),
