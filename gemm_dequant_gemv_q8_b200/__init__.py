@@ -7,6 +7,8 @@ cannot be loaded every call raises -- there is no fallback of any kind.
 
 The functions keep the C names (``qlin_pack_weights``, ``qlin_gemv``, ...).  They take torch
 tensors, check dtype/device/contiguity, and pass raw pointers, sizes and the current stream.
+The calls of the KV cache and the attention are marshalled by a native module built beside the
+library (``_qlin_torch.so``, csrc/torch_binding.cpp): ctypes would take longer than they run.
 """
 from __future__ import annotations
 

@@ -182,11 +182,11 @@ template <typename X, typename Y, int D, int TURN, bool APPEND>
 __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs a) {
     constexpr int LPH = D / 8, HPW = 32 / LPH;         // lanes a head, heads a warp at once
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * kRopeWarps + warp;
-    const int64_t t = item / a.chunks;
+    const uint32_t item = blockIdx.x * kRopeWarps + warp;  // below 2^30: 2^20 tokens of 2 x 128 + 2 x 256 warps at most
+    const int64_t t = item / (uint32_t)a.chunks;
     if (t >= a.T) return;
     // this warp's heads: chunks of queries, then of keys, then of values
-    int c = (int)(item - t * a.chunks);
+    int c = (int)(item - (uint32_t)t * (uint32_t)a.chunks);
     constexpr int KVH = APPEND ? kQuantHeadsPerWarp : kHeadsPerWarp;
     const int cq = APPEND && !a.q ? 0 : (a.Hq + kHeadsPerWarp - 1) / kHeadsPerWarp, ck = (a.Hkv + KVH - 1) / KVH;
     const int kind = c < cq ? 0 : c < cq + ck ? 1 : 2;
@@ -290,9 +290,9 @@ template <typename Y, int D>
 __global__ void __launch_bounds__(256) kv_gather_kernel(Cache cache, int64_t T, const int32_t* slots, Y* k, Y* v,
                                                         unsigned* status) {
     constexpr int LPH = D / 8;
-    const int64_t per = (int64_t)cache.Hkv * LPH;  // lanes a token
+    const int per = cache.Hkv * LPH;  // lanes a token
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t t = i / per;
+    const int64_t t = (i >> 32) == 0 ? (int64_t)((uint32_t)i / (uint32_t)per) : i / per;
     if (t >= T) return;
     const int rem = (int)(i - t * per), h = rem / LPH, d0 = (rem % LPH) * 8;
     const int slot = slots[t];

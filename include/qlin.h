@@ -1,8 +1,9 @@
 /*
  * qlin.h -- C ABI of libqlin, a B200 (sm_100a) library for the decode-step linear layer over
  * block-quantized weights: fused dequantize-and-multiply of GGUF Q8_0 / Q4_0 / Q4_K / Q6_K blocks and
- * NVFP4 / MXFP4 tensors against a small batch of activation rows, the routed MoE expert projections, and
- * an NVFP4 prefill-chunk GEMM on the tcgen05 tensor cores.
+ * NVFP4 / MXFP4 tensors against a small batch of activation rows, the routed MoE expert projections,
+ * an NVFP4 prefill-chunk GEMM on the tcgen05 tensor cores, and between the projections the query / key
+ * norm and rotation, a paged NVFP4 KV cache and the attention over it.
  *
  * What the operations compute comes from the pages describing the "imp" engine (README
  * "Features" table, rows "Quantization", "Architectures" and "sm_120a kernels"; README "Why this
@@ -29,7 +30,8 @@
  *     Where the counters sit depends on the call's shapes for qlin_gemv, qlin_gemv_chain and
  *     qlin_moe_experts: reuse their workspace only for calls with the same op and shapes (or zero
  *     it again).  qlin_gemm_chunk and qlin_moe_prefill keep theirs at fixed places or clear them
- *     themselves, so any later call may reuse their workspace.
+ *     themselves, so any later call may reuse their workspace.  qlin_attn_kv4's serves any later
+ *     qlin_attn_kv4 call that it is large enough for.
  */
 #ifndef QLIN_H
 #define QLIN_H
@@ -498,7 +500,8 @@ size_t qlin_attn_kv4_workspace_bytes(const qlin_kv_cache* cache, int B, int max_
  *       be reused by any later qlin_attn_kv4 call on the same stream for which it is large enough
  * A sequence with n outside [0, max_q], rows outside [0, total_q) or L outside [0, max_pages * page] is
  * skipped; a page number outside [0, n_pages) counts as masked places.  Both set the status word
- * (QLIN_ERR_INVALID_ARG).  Results are the same from run to run. */
+ * (QLIN_ERR_INVALID_ARG).  Results are the same from run to run.  No CTA waits for another; the waits
+ * within one are bounded by 2 s each, and after QLIN_ERR_TIMEOUT ws has to be zero-filled again. */
 qlin_status_t qlin_attn_kv4(const qlin_kv_cache* cache, const void* q, int64_t ldq, const int32_t* block_table,
                             int64_t ldb, int max_pages, const int32_t* seq_lens, const int32_t* cu_q, int B,
                             int max_q, int64_t total_q, int Hq, float scale, int window, void* out, int64_t ldo,
@@ -506,7 +509,8 @@ qlin_status_t qlin_attn_kv4(const qlin_kv_cache* cache, const void* q, int64_t l
 
 /* Read and clear the sticky device status word of a workspace (synchronises `stream`).
  * Returns QLIN_OK, QLIN_ERR_TIMEOUT if a bounded device wait gave up since the last check, or
- * QLIN_ERR_INVALID_ARG if qlin_moe_experts met an invalid or repeated expert id. */
+ * QLIN_ERR_INVALID_ARG if a call met something invalid in device memory: an invalid or repeated expert
+ * id (qlin_moe_experts), a position, slot, page number or sequence out of range (the cache's calls). */
 qlin_status_t qlin_ws_status(void* ws, qlin_stream_t stream);
 
 /* Test and fault-injection aid: set the budget, in nanoseconds, of the bounded device waits between
