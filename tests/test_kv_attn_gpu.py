@@ -667,6 +667,74 @@ def test_calls_on_two_streams_at_once():
     assert torch.equal(qk[0], want[0][0])
 
 
+def test_strided_rows_and_tables():
+    # rows of x, of the block table and of the outputs as parts of wider ones, for one sequence and for several
+    Hq, Hkv, D, page = 4, 2, 64, 16
+    W = (Hq + 2 * Hkv) * D
+    for B in (1, 3):
+        T = 5 * B
+        wide = torch.randn(T, W + 16, generator=gen(30 + B)).cuda()
+        x = wide[:, 8:8 + W]
+        slots = torch.randperm(B * 16, generator=gen(31))[:T].int().cuda()
+        a, b = q.kv_cache(B, page, Hkv, D), q.kv_cache(B, page, Hkv, D)
+        qa = q.qlin_kv_append(a, x, Hq, None, slots)
+        qw = torch.full((T, Hq * D + 8), 7.0, dtype=BF16, device="cuda")
+        q.qlin_kv_append(b, x.contiguous(), Hq, None, slots, q=qw[:, :Hq * D])
+        assert torch.equal(a.data, b.data) and torch.equal(qa.flatten(1), qw[:, :Hq * D]) and (qw[:, Hq * D:] == 7).all()
+        tab = torch.full((B, 9), -1, dtype=torch.int32, device="cuda")
+        tab[:, 3] = torch.arange(B, device="cuda")
+        lens = torch.full((B,), 16, dtype=torch.int32, device="cuda")
+        cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * 5
+        # slots that no token was appended to hold zeros: places like any other
+        o1 = q.qlin_attn_kv4(a, qw[:, :Hq * D].unflatten(1, (Hq, D)), tab[:, 3:4], lens, cu, 5)
+        o2 = q.qlin_attn_kv4(a, qa, tab[:, 3:4].contiguous(), lens, cu, 5)
+        assert torch.equal(o1, o2) and torch.isfinite(o1.float()).all()
+
+
+def test_decode_loop_in_one_graph():
+    """The append, the attention and the read-back of a decode step captured once and replayed for many steps, positions,
+    slots and lengths renewed in place, against the same calls made one by one on another cache."""
+    Hq, Hkv, D, page, B, steps = 8, 2, 128, 16, 3, 40
+    W = (Hq + 2 * Hkv) * D
+    xs = torch.randn(steps, B, W, generator=gen(40)).cuda()
+    cs, w = ref.table(200, D).cuda(), [(1 + 0.2 * torch.randn(D, generator=gen(i))).cuda() for i in (41, 42)]
+    start = [0, 100, 31]
+    table = torch.randperm(27, generator=gen(43)).view(3, 9).int().cuda()
+    past = torch.randn(B, 144, W, generator=gen(44)).cuda()
+    caches = [q.kv_cache(27, page, Hkv, D, 0.5, 2.0) for _ in range(2)]
+    place = lambda b, p: table[b, p // page] * page + p % page  # noqa: E731
+    for c in caches:
+        for b in range(B):
+            if start[b]:
+                p = torch.arange(start[b], device="cuda")
+                q.qlin_kv_append(c, past[b, :start[b]], Hq, p.int(), place(b, p).int(), cs, *w)
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    ws = q.workspace(q.qlin_attn_kv4_workspace_bytes(caches[0], B, 1, Hq))
+    x, pos, slots, lens = torch.zeros(B, W, device="cuda"), cu[:B].clone(), cu[:B].clone(), cu[:B].clone()
+
+    def renew(s):
+        x.copy_(xs[s])
+        pos.copy_(torch.tensor([n + s for n in start], dtype=torch.int32))
+        slots.copy_(torch.stack([place(b, start[b] + s) for b in range(B)]))
+        lens.copy_(torch.tensor([n + s + 1 for n in start], dtype=torch.int32))
+
+    def step(c):
+        qo = q.qlin_kv_append(c, x, Hq, pos, slots, cs, *w, ws=ws)
+        o = q.qlin_attn_kv4(c, qo, table, lens, cu, 1, ws=ws)
+        return [o, *q.qlin_kv_gather(c, slots, ws=ws)]
+
+    renew(0)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        out = step(caches[0])
+    for s in range(steps):
+        renew(s)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, step(caches[1]))), s
+    assert q.qlin_ws_status(ws) == 0 and torch.equal(caches[0].data, caches[1].data)
+
+
 def test_calls_without_rows():
     D, page = 64, 16
     cache = q.kv_cache(2, page, 1, D)
