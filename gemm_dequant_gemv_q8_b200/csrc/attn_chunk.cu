@@ -432,6 +432,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             for (int c = 0; c < D; c += 32) {
                 float v[32];
                 uint32_t raw[32];
+                __syncwarp();
                 if (active && ok) {
                     ld32(to + c, raw);
                     ld_wait(raw);

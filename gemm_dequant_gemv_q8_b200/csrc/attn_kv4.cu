@@ -28,8 +28,8 @@ namespace kv {
 // The cache has to be read once, and is; what bounds the kernel is the arithmetic that dequantizes it (one conversion a
 // byte and one product a pair of values: ALU pipe 50% busy, an instruction issued in 56% of the active cycles) beside
 // some 9 us of start and end (launch, lengths and pages, the joining).  64 sequences of up to 8192 tokens (8 kv heads of
-// 128, 374 MB): 102 us, 3.7 TB/s; the copies alone 67, without V's arithmetic 80, without K's 89.  1 x 131071 39 us
-// (3.9 TB/s); 16 x 4096 ragged (heads of 64, 24 MB) 20; 1 x 1000 9.5.  Warps: 16 give 102 / 41 / 20.1 us on the first
+// 128, 374 MB): 104 us, 3.6 TB/s; the copies alone 67, without V's arithmetic 80, without K's 89.  1 x 131071 40 us
+// (3.8 TB/s); 16 x 4096 ragged (heads of 64, 24 MB) 20; 1 x 1000 9.5.  Warps: 16 give 102 / 41 / 20.1 us on the first
 // three (before the shares), 12 105 / 44 / 20.8, 8 114 / 47 / 21.1.
 template <int D, int NT>
 struct Dec {
@@ -327,7 +327,8 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         for (int j = 0; j < tiles; ++j, tok0 += W * TILE) {
             const int s = stage;
             if (failed && done >= issued) break;
-            if (!mbar_wait_bounded(&bars[warp * S + s], phase, failed ? 50000000ull : 2000000000ull)) {
+            // the warp goes on, or gives up, as one
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[warp * S + s], phase, failed ? 50000000ull : 2000000000ull))) {
                 if (lane == 0) atomicOr(a.status, 1u);
                 failed = true;
                 mine = issued;  // nothing more is copied; what is in flight is waited for
