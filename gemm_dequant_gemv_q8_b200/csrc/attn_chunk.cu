@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                         top = fmaxf(t0, t1);
                     }
                     top = top == -INFINITY ? top : __fmul_rn(top, rs);
-                    if (__any_sync(0xffffffffu, top > m + 8.f)) {
+                    if (__any_sync(0xffffffffu, __fsub_rn(top, m) > 8.f)) {  // m + 8 would be rounded up to m + 16 above 2^27
                         const float mn = fmaxf(m, top);
                         const float f = m == -INFINITY ? 0.f : ex2(m - mn);
                         m = mn;

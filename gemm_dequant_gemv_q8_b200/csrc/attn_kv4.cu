@@ -404,7 +404,8 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                 }
                 // The reference that is taken off the scores follows the maximum only when that has grown by 2^8: the
                 // probabilities then reach 2^8, which fp16 holds; the maximum goes round the lanes, and O is rescaled,
-                // only then.
+                // only then.  (The growth is the difference, exact where it matters; m + 8 would be rounded up to m + 16
+                // above 2^27.)
                 float mx[NT][2];
                 bool grow = false;
 #pragma unroll
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
 #pragma unroll
                         for (int gr = 1; gr < NG; ++gr) v = fmaxf(v, fmaxf(sc[gr][nt][c], sc[gr][nt][2 + c]));
                         mx[nt][c] = v;
-                        grow |= __fmul_rn(v, rs[nt][c]) > m[nt][c] + 8.f;
+                        grow |= __fsub_rn(__fmul_rn(v, rs[nt][c]), m[nt][c]) > 8.f;
                     }
                 if (__any_sync(0xffffffffu, grow)) {
                     bool big = false;

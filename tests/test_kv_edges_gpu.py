@@ -1,0 +1,59 @@
+"""Edges of the cache's and the attention's calls: far tails of a softmax, scores near the limits of 32 bits, NaN and
+junk in the cache, the range of the norms, pages that are missing, every token counted once."""
+import math
+
+import pytest
+import torch
+
+import gemm_dequant_gemv_q8_b200 as q
+import kv_reference as ref
+from test_kv_attn_gpu import BF16, F32, attn_case, gen, rope_tol, run_attn
+
+pytestmark = pytest.mark.gpu
+
+
+def exact_cache(k, v, page):
+    """A cache of one sequence whose token t has the key k[t] and the value v[t], (L, Hkv, D) each of exact NVFP4 values
+    (0 and 6, or 4 beside a 6), at slots 0 .. L - 1."""
+    L, Hkv, D = k.shape
+    cache = q.kv_cache(-(-L // page), page, Hkv, D)
+    for t0 in range(0, L, 1 << 18):
+        x = torch.cat([k[t0:t0 + (1 << 18)].flatten(1), v[t0:t0 + (1 << 18)].flatten(1)], 1)
+        q.qlin_kv_append(cache, x, 0, None, torch.arange(t0, t0 + len(x), dtype=torch.int32, device="cuda"))
+    return cache
+
+
+def call(cache, L, nq, Hq, B=1, scale=None, query=None, window=0):
+    """B sequences over the same pages, nq queries each, all alike: `query` gives a query's values, 0 elsewhere."""
+    D, n = cache.D, -(-L // cache.page)
+    qs = torch.zeros(B * nq, Hq, D, dtype=BF16, device="cuda")
+    for d, x in (query or {}).items():
+        qs[..., d] = x
+    table = torch.arange(n, dtype=torch.int32, device="cuda").expand(B, n).contiguous()
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * nq
+    ws = q.workspace(q.qlin_attn_kv4_workspace_bytes(cache, B, nq, Hq))
+    o = q.qlin_attn_kv4(cache, qs, table, lens, cu, nq, scale, window=window, ws=ws)
+    assert q.qlin_ws_status(ws) == 0
+    return o
+
+
+@pytest.mark.parametrize("nq", [1, 70])
+def test_scores_of_a_hundred_million(nq):
+    # Between 2^27 and 2^28 a score rises by one step of its last bit, 16, whose half is 8.  All values are 6, and so is the
+    # output, whatever the weights.
+    f = lambda x: torch.tensor(x, dtype=torch.float32)  # noqa: E731
+    for i in range(100):  # a scale that puts the two scores at odd and even last bits, with the kernels' roundings
+        scale = f(1.5 * 2.0 ** 27 / 1.4426950408889634 / 6 * (1 + i * 2.0 ** -22))
+        rs = scale * f(1.4426950408889634) * f(2.0 ** -14)
+        lo, hi = f(6 * 2.0 ** 14) * rs, f(6 * 2.0 ** 14 + 2.0 ** -7) * rs
+        if hi - lo == 16 and lo + 8 == hi:
+            break
+    assert hi - lo == 16 and lo + 8 == hi
+    D, page, L, B = 64, 64, 4096, 64
+    k, v = torch.zeros(L, 1, D, device="cuda"), torch.full((L, 1, D), 6.0, device="cuda")
+    k[..., 0] = k[..., 17] = 6
+    k[..., 16] = torch.where(torch.arange(L, device="cuda") // 512 % 2 == 1, 4.0, 0.0)[:, None]
+    cache = exact_cache(k, v, page)
+    o = call(cache, L, nq, 1, B, scale.item(), {0: 1.0, 16: 2.0 ** -23})
+    assert (o == 6).all()
