@@ -14,7 +14,8 @@
 //                   next S_B: the tensor cores work for one tile while the other's softmax runs;
 //   warp 13       : deals out the units: a ring of descriptions in shared memory that the others read
 //                   (warps 14 and 15 are idle: registers are dealt out by four warps).
-// The exponent's reference follows the running maximum only when that has grown by 2^8, so O is rarely rescaled.
+// The exponents' reference follows the running maximum only when that has grown by 2^8 (kBelow, kGrow), so O is rarely
+// rescaled.
 //
 // 2 x 2047 queries of 8189 tokens (32 heads of 128): 381 us, 863 TFLOP/s; 8192 of 8192: 608 us, 905 TFLOP/s.  The bound is
 // the chain of a tile of rows: 1.55 us of softmax, then 0.8 us until its next scores are there, while the tensor cores
@@ -345,8 +346,8 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                         top = fmaxf(t0, t1);
                     }
                     top = top == -INFINITY ? top : __fmul_rn(top, rs);
-                    if (__any_sync(0xffffffffu, __fsub_rn(top, m) > 8.f)) {  // m + 8 would be rounded up to m + 16 above 2^27
-                        const float mn = fmaxf(m, top);
+                    if (__any_sync(0xffffffffu, __fsub_rn(top, m) > kGrow)) {  // the difference: a sum would be rounded up where m is large
+                        const float mn = fmaxf(m, __fsub_rn(top, kBelow));
                         const float f = m == -INFINITY ? 0.f : ex2(m - mn);
                         m = mn;
                         l *= f;
@@ -365,10 +366,10 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                     const float ref = m == -INFINITY ? 0.f : m;
                     float2 sum = make_float2(0.f, 0.f);
                     // the probabilities go where scores have been read already
-                    if (edge || __any_sync(0xffffffffu, fabsf(ref) >= 0x1p24f)) {
-                        // The careful form rounds twice, as the reference does: the largest score's exponent is 0 whatever
-                        // its size.  One rounding (below) leaves up to half an ulp of the reference there, less than 1
-                        // below 2^24, the same for the whole row.
+                    if (edge || __any_sync(0xffffffffu, fabsf(ref) >= 0x1p20f)) {
+                        // The careful form rounds twice, as the reference does: no score's exponent is above kGrow whatever
+                        // its size.  One rounding (below) leaves up to half an ulp of the score there, at most 2^-4 below
+                        // 2^20, the same for the whole row.
                         if (!edge) ld_wait(u0);
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {

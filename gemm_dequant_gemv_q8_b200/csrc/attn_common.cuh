@@ -87,6 +87,12 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+// What is taken off a row's scores (its reference) is set kBelow under the largest score seen, and set anew only when a score
+// has come to lie more than kGrow above it: O is rarely rescaled.  A row's largest probability is then 2^7 to 2^15 (2^15.1
+// with the rounding of a product below 2^20), which fp16 holds, and those that it rounds to 0 lie 2^32 and more below the
+// largest: of 2^20 equal tokens under one large one, less than half a step of bf16 is lost.  The sum counts them all.
+constexpr float kBelow = 7.f, kGrow = 15.f;
+
 // Exponent of a query row's largest magnitude, kept where both 2^(14 - e) and 2^(e - 14) are normal numbers: the row
 // times 2^(14 - e) (with the sign of the scale) is fp16 with its largest magnitude in [2^14, 2^15), exact but for
 // values 2^28 below it, and |scale| 2^(e - 14) takes the scores to the exponents of 2.

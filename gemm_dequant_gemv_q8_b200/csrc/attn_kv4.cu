@@ -303,8 +303,8 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
         const int64_t next = t0 + warp + (int64_t)done * W, end = s1 < t1 ? s1 : t1;
         const int tiles = next < end ? (int)((end - next + W - 1) / W) : 0;
         const bool any = tiles > 0;
-        float nref[NT][2];  // what is added to the exponents: -m, 0 where nothing has been seen
-        bool huge = false;  // some |m| of the warp is 2^24 or more
+        float nref[NT][2];  // what is added to the exponents: -m (m the reference), 0 where nothing has been seen
+        bool huge = false;  // some |m| of the warp is 2^20 or more
         if (any) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -402,10 +402,8 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                                 sc[gr][nt][c] = sees ? sc[gr][nt][c] : -INFINITY;
                             }
                 }
-                // The reference that is taken off the scores follows the maximum only when that has grown by 2^8: the
-                // probabilities then reach 2^8, which fp16 holds; the maximum goes round the lanes, and O is rescaled,
-                // only then.  (The growth is the difference, exact where it matters; m + 8 would be rounded up to m + 16
-                // above 2^27.)
+                // The maximum goes round the lanes, and O is rescaled, only where the reference has to follow it (kGrow).  The
+                // growth is the difference, exact where it matters: a sum would be rounded up where scores are large.
                 float mx[NT][2];
                 bool grow = false;
 #pragma unroll
@@ -416,7 +414,7 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
 #pragma unroll
                         for (int gr = 1; gr < NG; ++gr) v = fmaxf(v, fmaxf(sc[gr][nt][c], sc[gr][nt][2 + c]));
                         mx[nt][c] = v;
-                        grow |= __fsub_rn(__fmul_rn(v, rs[nt][c]), m[nt][c]) > 8.f;
+                        grow |= __fsub_rn(__fmul_rn(v, rs[nt][c]), m[nt][c]) > kGrow;
                     }
                 if (__any_sync(0xffffffffu, grow)) {
                     bool big = false;
@@ -429,11 +427,11 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                            const float mn = fmaxf(m[nt][c], v == -INFINITY ? v : __fmul_rn(v, rs[nt][c]));
+                            const float mn = fmaxf(m[nt][c], v == -INFINITY ? v : __fsub_rn(__fmul_rn(v, rs[nt][c]), kBelow));
                             f[c] = m[nt][c] == -INFINITY ? 0.f : ex2(m[nt][c] - mn);
                             m[nt][c] = mn;
                             nref[nt][c] = mn == -INFINITY ? 0.f : -mn;
-                            big |= fabsf(nref[nt][c]) >= 0x1p24f;
+                            big |= fabsf(nref[nt][c]) >= 0x1p20f;
                             l[nt][c] *= f[c];
                         }
 #pragma unroll
@@ -443,8 +441,8 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                     }
                     huge = __any_sync(0xffffffffu, big);
                 }
-                // One rounding leaves up to half an ulp of the reference on the largest score's exponent, less than 1 below
-                // 2^24, the same for the whole row; beyond that two, as the reference has, make it 0.
+                // One rounding leaves up to half an ulp of the largest score on its exponent, at most 2^-4 below 2^20, the
+                // same for the whole row; beyond that two, as the reference has, leave none.
                 float p[NG][NT][4];
                 if (edge || huge) {
 #pragma unroll

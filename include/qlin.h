@@ -488,7 +488,9 @@ size_t qlin_attn_kv4_workspace_bytes(const qlin_kv_cache* cache, int B, int max_
  *   q, out : total_q rows of Hq * D bf16, row strides ldq and ldo elements, 16-byte aligned rows; rows
  *       outside cu_q[0] .. cu_q[B] are left as they are; out is no part of q.  The products are exact
  *       values of K and V with q and with probabilities in fp16; scores, softmax sums and outputs are
- *       fp32, rounded once.  Scores have to stay finite in fp32, or their row is NaN
+ *       fp32, rounded once.  A probability is off by 2^-32 of its row's largest at most where fp16 has no
+ *       normal numbers for it: L tokens far below one that takes nearly all lose up to L * 2^-32 of it.
+ *       Scores have to stay finite in fp32, or their row is NaN
  *   block_table : B rows of int32 page numbers, row stride ldb, max_pages columns (max_pages * page <=
  *       2^26): token t of sequence b is token t % page of page block_table[b * ldb + t / page].  Sequences
  *       may share pages.  Numbers of pages with no token that a query of the sequence sees (behind its

@@ -38,6 +38,28 @@ def call(cache, L, nq, Hq, B=1, scale=None, query=None, window=0):
     return o
 
 
+@pytest.mark.parametrize("octaves", [18.0, 22.5, 25.5, 27.0])
+@pytest.mark.parametrize("L,B,nq,Hkv", [(65536, 256, 1, 8), (65536, 1, 8192, 8), (131072, 1, 1, 1)])
+def test_a_tail_far_below_the_largest_score_keeps_its_mass(L, B, nq, Hkv, octaves):
+    # The first token takes nearly all and has the value 0; the others, 6 each, lie `octaves` below it.  Query at place p:
+    # 6 p 2^-octaves / (1 + p 2^-octaves).
+    D, page = 64, 64
+    k, v = torch.zeros(L, Hkv, D, device="cuda"), torch.full((L, Hkv, D), 6.0, device="cuda")
+    k[0, :, 0], v[0] = 6, 0
+    scale = octaves * math.log(2) / 6
+    o = call(exact_cache(k, v, page), L, nq, Hkv, B, scale, {0: 1.0}).double().cpu()
+    p = torch.arange(L - nq, L, dtype=torch.float64).repeat(B)[:, None, None]
+    r = p * 2.0 ** -octaves
+    want = (6 * r / (1 + r)).expand_as(o)
+    A = octaves * math.log(2)
+    e = 2 * (2 * D + 4) * 2.0 ** -24 * A
+    rel = 2 * (math.expm1(e) + 2.0 ** -21) + 2.0 ** -11 + (4 * L + 32) * 2.0 ** -24
+    tol = want * rel + 6 * p * 2.0 ** -32
+    tol = tol + 2.0 ** -8 * (want + tol)
+    err = (o - want).abs()
+    assert (err <= tol).all(), float((err / tol).max())
+
+
 @pytest.mark.parametrize("nq", [1, 70])
 def test_scores_of_a_hundred_million(nq):
     # Between 2^27 and 2^28 a score rises by one step of its last bit, 16, whose half is 8.  All values are 6, and so is the
