@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             const int r = it.base + srow;
             const int64_t slot = it.parts > 1 ? (int64_t)(it.tail * it.parts + it.part) : 0;
             float* part = a.parts + slot * kRows * (D + 2);  // [D / 4][256 rows] of four values, then [256] {m, l}
-            const float inv = l == 0.f ? 0.f : a.cache.v_scale / l;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             __nv_bfloat16* dst = a.out + (it.row0 + group_div(a, r)) * a.ldo + (int64_t)(it.h * a.G + group_mod(a, r)) * D;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                         uint32_t u[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[i + 2 * q] * inv, v[i + 2 * q + 1] * inv);
+                            const __nv_bfloat162 b2 = out_pair(a, v[i + 2 * q], v[i + 2 * q + 1], inv);
                             u[q] = *reinterpret_cast<const uint32_t*>(&b2);
                         }
                         *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(u[0], u[1], u[2], u[3]);
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                         factor[s * kRows] = f;
                         lj += ml.y * f;
                     }
-                    const float invj = lj == 0.f ? 0.f : a.cache.v_scale / lj;
+                    const float invj = lj == 0.f ? 0.f : 1.f / lj;
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
                         float4 acc[4] = {};
@@ -517,8 +517,8 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                         uint32_t u[8];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[i].x * invj, acc[i].y * invj);
-                            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[i].z * invj, acc[i].w * invj);
+                            const __nv_bfloat162 lo = out_pair(a, acc[i].x, acc[i].y, invj);
+                            const __nv_bfloat162 hi = out_pair(a, acc[i].z, acc[i].w, invj);
                             u[2 * i] = *reinterpret_cast<const uint32_t*>(&lo), u[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&hi);
                         }
                         *reinterpret_cast<uint4*>(dst + c) = make_uint4(u[0], u[1], u[2], u[3]);

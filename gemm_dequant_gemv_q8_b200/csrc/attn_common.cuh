@@ -112,5 +112,11 @@ __device__ __forceinline__ uint32_t scaled_f16x2(uint32_t w, float up) {
     return pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
 }
 
+// Two output values: sums of P V times the reciprocal of P's sum, then the cache's scale (over the sum it need not be a
+// normal number).
+__device__ __forceinline__ __nv_bfloat162 out_pair(const AttnArgs& a, float x, float y, float inv) {
+    return __floats2bfloat162_rn(x * inv * a.cache.v_scale, y * inv * a.cache.v_scale);
+}
+
 }  // namespace kv
 }  // namespace qlin

@@ -586,11 +586,11 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                     sum += f * ml.y;
                 }
                 if (whole) {
-                    const float inv = sum == 0.f ? 0.f : a.cache.v_scale / sum;
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
                     const int rr = rb * C::kRows + nt * 8 + r;
                     *reinterpret_cast<__nv_bfloat162*>(a.out + (qrow + group_div(a, rr)) * a.ldo +
                                                        (int64_t)(h * a.G + group_mod(a, rr)) * D + 2 * pair) =
-                        __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+                        out_pair(a, acc.x, acc.y, inv);
                 } else {
                     __stcg(reinterpret_cast<float2*>(part + (nt * 8 + r) * D + 2 * pair), acc);
                     if (pair == 0) __stcg(reinterpret_cast<float2*>(part + C::kRows * D + 2 * (nt * 8 + r)), make_float2(M, sum));
@@ -679,12 +679,12 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                         __syncthreads();
                     }
                     if (sp == 0 && r < rows) {
-                        const float inv = sum == 0.f ? 0.f : a.cache.v_scale / sum;
+                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
                         const int rr = rb * C::kRows + r;
                         __nv_bfloat16* dst = a.out + (qrow + group_div(a, rr)) * a.ldo + (int64_t)(h * a.G + group_mod(a, rr)) * D + lane * V;
 #pragma unroll
                         for (int k = 0; k < V; k += 2)
-                            *reinterpret_cast<__nv_bfloat162*>(dst + k) = __floats2bfloat162_rn(acc[k] * inv, acc[k + 1] * inv);
+                            *reinterpret_cast<__nv_bfloat162*>(dst + k) = out_pair(a, acc[k], acc[k + 1], inv);
                     }
                 }
             }

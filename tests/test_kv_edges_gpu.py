@@ -79,3 +79,17 @@ def test_scores_of_a_hundred_million(nq):
     cache = exact_cache(k, v, page)
     o = call(cache, L, nq, 1, B, scale.item(), {0: 1.0, 16: 2.0 ** -23})
     assert (o == 6).all()
+
+
+@pytest.mark.parametrize("nq", [1, 70])
+@pytest.mark.parametrize("vs", [2.0 ** -120, 2.0 ** -126, 2.0 ** -136])
+def test_the_smallest_value_scales(nq, vs):
+    # V is 6 * 448 everywhere, the largest value of the cache, so the output is that times the scale: a normal number in bf16
+    # although the scale over the softmax sum is none in fp32.
+    D, page, L = 64, 64, 30000
+    v = torch.full((L, 2, D), 6.0 * 448, device="cuda")
+    cache = exact_cache(torch.zeros_like(v), v, page)
+    small = q.KVCache(cache.data, page, 2, D, 1.0, vs)
+    o = call(small, L, nq, 4).double()
+    want = 6 * 448 * vs
+    assert ((o - want).abs() <= (2.0 ** -8 + 8 * 2.0 ** -24) * want).all()
