@@ -434,7 +434,8 @@ def _on(stream, device, fn, *args):
 def qlin_qk_norm_rope(x, Hq, Hkv, D, positions=None, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, rot=None,
                       flags=QLIN_ROPE_HALVES, q=None, k=None, ydt=QLIN_BF16, ws=None, stream=None):
     """Norm (where a weight is given) and rotation of the query and key heads at the front of x's rows
-    (T, >= (Hq + Hkv) * D).  Returns (q, k) as (T, heads, D); q and k may be x's own heads."""
+    (T, >= (Hq + Hkv) * D).  rot, the rotated values of a head, is cos_sin's columns, or 0 without a table, where it is not
+    given.  Returns (q, k) as (T, heads, D); q and k may be x's own heads."""
     if stream is not None:
         return _on(stream, x.device, qlin_qk_norm_rope, x, Hq, Hkv, D, positions, cos_sin, q_weight, k_weight, eps, rot, flags, q, k, ydt, ws)
     if ws is None:

@@ -140,10 +140,12 @@ struct Where {
 // cos_sin, q_weight, k_weight, eps, rot, flags
 qlin_qk_params params(PyObject* const* a, int D, int dev) {
     qlin_qk_params p = {};
+    if (a[4] != Py_None) p.rot = small(a[4]);  // without a table the library refuses what is not 0
     if (a[0] != Py_None) {
         const at::Tensor& t = on_device(a[0], "cos_sin", at::kFloat, dev);
         if (t.dim() != 2 || !t.is_contiguous()) fail(PyExc_ValueError, "%s must be a contiguous (positions, rot) tensor", "cos_sin");
-        p.rot = a[4] == Py_None ? (int)t.size(1) : small(a[4]);
+        if (t.size(1) > INT32_MAX) fail(PyExc_ValueError, "%s is too large", "cos_sin");
+        if (a[4] == Py_None) p.rot = (int)t.size(1);
         if (p.rot && t.size(1) != p.rot) fail(PyExc_ValueError, "%s must be (positions, rot)", "cos_sin");
         p.cos_sin = static_cast<const float*>(t.data_ptr());
         p.n_pos = t.size(0);

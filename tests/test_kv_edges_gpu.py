@@ -93,3 +93,16 @@ def test_the_smallest_value_scales(nq, vs):
     o = call(small, L, nq, 4).double()
     want = 6 * 448 * vs
     assert ((o - want).abs() <= (2.0 ** -8 + 8 * 2.0 ** -24) * want).all()
+
+
+def test_rotation_without_a_table_is_refused():
+    D, page = 64, 16
+    x = torch.randn(3, 4 * D, generator=gen(1)).cuda()
+    pos = torch.arange(3, dtype=torch.int32).cuda()
+    cache = q.kv_cache(1, page, 1, D)
+    for f in (lambda r: q.qlin_qk_norm_rope(x, 2, 1, D, pos, None, rot=r), lambda r: q.qlin_kv_append(cache, x, 2, pos, pos, None, rot=r)):
+        f(0)
+        for r in (16, D, -16):
+            with pytest.raises(q.QlinError) as e:
+                f(r)
+            assert e.value.status == 1
