@@ -148,8 +148,10 @@ __device__ __forceinline__ void norm_rope(float (&v)[8], bool norm, const float 
 }
 
 // The scale byte of a block whose largest magnitude is m, under scale g: E4M3(m / (6 g)).  div_by_recip gives the correctly
-// rounded quotient where nothing over- or underflows on the way; g6 = 6 g and its reciprocal y6 are the same for all.
+// rounded quotient where nothing over- or underflows on the way; g6 = 6 g and its reciprocal y6 are the same for all.  m is
+// NaN where a block holds nothing else: scale 0, for a NaN in the cache would reach the queries that do not see it.
 __device__ __forceinline__ uint8_t block_scale(float m, float g6, float y6) {
+    m = fmaxf(m, 0.f);
     const bool plain = g6 >= 0x1p-60f && g6 <= 0x1p60f && m <= 0x1p60f;
     return e4m3_rne_sat(plain ? div_by_recip(m, g6, y6) : __fdiv_rn(m, g6));
 }

@@ -462,7 +462,8 @@ qlin_status_t qlin_qk_norm_rope(const void* x, qlin_dtype_t xdt, int64_t T, int6
  *   where that divisor is 0.
  * A key's fp32 value is the 64-bit result rounded once, so that its code does not depend on the order of
  * a sum: the same token gives the same bytes appended alone or in a chunk.  Infinite inputs saturate;
- * NaN inputs give some finite value.  Other slots of the cache are left as they are.
+ * NaN inputs (and a normed key with an infinite or NaN value) give some finite value, zeros where all 16
+ * of a block are NaN.  Other slots of the cache are left as they are.
  * Errors as above; a position outside [0, n_pos) or a slot outside [-1, n_pages * page) leaves the
  * token unwritten and sets the status word. */
 qlin_status_t qlin_kv_append(const qlin_kv_cache* cache, const void* x, qlin_dtype_t xdt, int64_t T, int64_t ldx,

@@ -106,3 +106,45 @@ def test_rotation_without_a_table_is_refused():
             with pytest.raises(q.QlinError) as e:
                 f(r)
             assert e.value.status == 1
+
+
+@pytest.mark.parametrize("xdt", [F32, BF16])
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("rot,inter", [(0, False), (128, False), (48, False), (64, True)])
+def test_append_of_nan_leaves_finite_values(xdt, norm, rot, inter):
+    T, Hq, Hkv, D, page = 9, 1, 2, 128, 16
+    x = torch.randn(T, (Hq + 2 * Hkv) * D, generator=gen(2))
+    x[0] = float("nan")
+    x[2, Hq * D:(Hq + Hkv) * D] = float("nan")
+    x[4, -D:] = float("nan")
+    x[5, -5] = float("nan")
+    x[6, Hq * D + 7] = float("nan")
+    x[7, Hq * D + 40] = float("inf")
+    x[8, Hq * D + 32:Hq * D + 48] = -float("inf")
+    cache = q.kv_cache(1, page, Hkv, D)
+    cs = ref.table(T, rot).cuda() if rot else None
+    w = torch.ones(D).cuda() if norm else None
+    slots = torch.arange(T, dtype=torch.int32).cuda()
+    q.qlin_kv_append(cache, x.to(xdt).cuda(), Hq, slots, slots, cs, w, w, flags=int(inter))
+    k, v = q.qlin_kv_gather(cache, slots, ydt=q.QLIN_F32)
+    assert torch.isfinite(k).all() and torch.isfinite(v).all()
+    assert (v[0] == 0).all() and (k[2] == 0).all() and (v[4, 1] == 0).all()  # blocks of nothing but NaN
+    kc, kb = ref.quantize(x[[1, 3, 4, 5, 6, 7, 8]].to(xdt)[:, -2 * D:].double().view(-1, Hkv, D)[:, :1].float(), 1.0)
+    assert torch.equal(v[[1, 3, 4, 5, 6, 7, 8]][:, :1].cpu(), ref.values(kc, kb).float())
+
+
+def test_a_nan_token_of_a_prompt_leaves_the_queries_before_it():
+    Hq, Hkv, D, page, T = 4, 2, 64, 16, 90
+    x = torch.randn(T, (Hq + 2 * Hkv) * D, generator=gen(3)).cuda()
+    bad = x.clone()
+    bad[70:] = float("nan")
+    slots = torch.arange(96, dtype=torch.int32).cuda()
+    w = torch.ones(D).cuda()
+    outs = []
+    for xi in (x, bad):
+        cache = q.kv_cache(6, page, Hkv, D)
+        qo = q.qlin_kv_append(cache, xi, Hq, None, slots[:T], None, w, w)
+        for nq in (T, 24):
+            outs.append(q.qlin_attn_kv4(cache, qo[T - nq:], torch.arange(6, dtype=torch.int32)[None].cuda(),
+                                        torch.tensor([T], dtype=torch.int32).cuda(), torch.tensor([0, nq], dtype=torch.int32).cuda(), nq))
+    assert torch.equal(outs[0][:70], outs[2][:70]) and torch.equal(outs[1][:4], outs[3][:4])
