@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
         // a tile that this thread has looked up: the groups of its tokens, or NULL (behind the end, a bad page)
         struct Place {
             const uint8_t *k, *v;
-            int left;  // tokens from V's first one to the context's end
+            int span;  // of V's 8 tokens those that may be seen: from the high half word up to the low one
             bool bad, some;
         };
         bool more = next_item();
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             return group_ptr<D>(a.cache, page, it.h, tok & ((1 << a.cache.page_log) - 1));
         };
         auto step = [&]() {  // on to the next tile
-            Place pl = {nullptr, nullptr, 0, false, false};
+            Place pl = {nullptr, nullptr, 8, false, false};
             if (more && ++tile >= ring[k % kItems].t1) {
                 more = next_item();
                 tile = more ? ring[k % kItems].t0 : 0;
@@ -573,7 +573,8 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
             pl.some = true;
             pl.k = group(tile * kTok + id, pl.bad);
             pl.v = vuse ? group(tile * kTok + vch * 8, ignored) : nullptr;
-            pl.left = ring[k % kItems].L - (tile * kTok + vch * 8);
+            const int tok = tile * kTok + vch * 8;
+            pl.span = (int)((uint32_t)max(ring[k % kItems].first - tok, 0) << 16) | min(ring[k % kItems].L - tok, 8);  // read where v is
             return pl;
         };
         struct Codes {
@@ -605,10 +606,13 @@ __global__ void __launch_bounds__(ch::kThreads, 1) attn_chunk_kernel(const AttnA
                     c.v[4 * i] = u.x, c.v[4 * i + 1] = u.y, c.v[4 * i + 2] = u.z, c.v[4 * i + 3] = u.w;
                 }
                 const uint2 u = __ldg(reinterpret_cast<const uint2*>(pl.v + v_scale_off(D) + vblk * 16 + r));
-                // places behind the end hold anything: scale 0, so that 0 * value is 0
-                const int left = pl.left;
-                c.vs[0] = left >= 4 ? u.x : u.x & ((1u << (8 * left)) - 1u);
-                c.vs[1] = left >= 8 ? u.y : left <= 4 ? 0u : u.y & ((1u << (8 * (left - 4))) - 1u);
+                c.vs[0] = u.x, c.vs[1] = u.y;
+                if (pl.span != 8) {  // places that no row sees hold anything: scale 0, so that 0 * value is 0
+                    const int from = pl.span >> 16, to = pl.span & 0xffff;  // to > 0: some of the 8 are in the context
+                    uint64_t keep = ~(uint64_t)0 >> (8 * (8 - to));
+                    keep = from >= 8 ? 0 : keep & (~(uint64_t)0 << (8 * from));
+                    c.vs[0] &= (uint32_t)keep, c.vs[1] &= (uint32_t)(keep >> 32);
+                }
             }
         };
         Codes c;

@@ -493,9 +493,11 @@ __global__ void __launch_bounds__(Dec<D, NT>::kWarps * 32, 1) attn_decode_kernel
                             v[k][0] = *reinterpret_cast<const uint32_t*>(gp + v_code_off(D) + blk * 128 + t * 32 + k * 8 + (g & 1) * 4);
                     }
                     uint32_t vs = *reinterpret_cast<const uint32_t*>(gp + v_scale_off(D) + blk * 16 + t * 4);
-                    if constexpr (edge) {  // places behind the end hold anything: scale 0, so that 0 * value is 0
+                    if constexpr (edge) {  // places that no query sees hold anything: scale 0, so that 0 * value is 0
                         const int left = (bad >> gr) & 1 ? 0 : qL - (tok0 + gr * kGroup + 4 * t);
                         vs = left >= 4 ? vs : left <= 0 ? 0u : vs & ((1u << (8 * left)) - 1u);
+                        const int before = first_seen(a, qn, qL) - (tok0 + gr * kGroup + 4 * t);
+                        vs = before <= 0 ? vs : before >= 4 ? 0u : vs & ~((1u << (8 * before)) - 1u);
                     }
                     const uint32_t f01 = e4m3x2_to_f16x2(vs & 0xffffu), f23 = e4m3x2_to_f16x2(vs >> 16);
 #pragma unroll

@@ -485,7 +485,8 @@ size_t qlin_attn_kv4_workspace_bytes(const qlin_kv_cache* cache, int B, int max_
  * L = seq_lens[b] tokens that counts the call's own (append them first): query i stands at place
  * p = L - n + i and sees the places t <= p, with window > 0 only those with t > p - window.  A query
  * that sees nothing (p < 0) gives a row of zeros.  Single tokens (n = 1) and prompt chunks are the same
- * call.  What the cache holds behind a sequence's end is never used, whatever its bits.
+ * call.  What the cache holds behind a sequence's end, or before the first place that a query of the
+ * sequence sees, is never used, whatever its bits.
  *   q, out : total_q rows of Hq * D bf16, row strides ldq and ldo elements, 16-byte aligned rows; rows
  *       outside cu_q[0] .. cu_q[B] are left as they are; out is no part of q.  The products are exact
  *       values of K and V with q and with probabilities in fp16; scores, softmax sums and outputs are

@@ -148,3 +148,21 @@ def test_a_nan_token_of_a_prompt_leaves_the_queries_before_it():
             outs.append(q.qlin_attn_kv4(cache, qo[T - nq:], torch.arange(6, dtype=torch.int32)[None].cuda(),
                                         torch.tensor([T], dtype=torch.int32).cuda(), torch.tensor([0, nq], dtype=torch.int32).cuda(), nq))
     assert torch.equal(outs[0][:70], outs[2][:70]) and torch.equal(outs[1][:4], outs[3][:4])
+
+
+@pytest.mark.parametrize("nq", [1, 5, 70])
+@pytest.mark.parametrize("window", [1, 40, 300])
+def test_attention_uses_nothing_before_the_window(nq, window):
+    # places that no query sees hold anything, in groups and pages with others that are seen too
+    lens, Hq, Hkv, D, page = [700, 333, 128], 8, 2, 128, 64
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, [nq] * 3, Hq, Hkv, D, page, 86)
+    want, _ = run_attn(c, page, Hkv, D, table, ln, cu, qs, window=window)
+    pages = c.view(-1, Hkv, page // 16, 18 * D)
+    for b, L in enumerate(lens):
+        for t in range(max(0, L - nq - window + 1)):
+            gr, r = pages[table[b, t // page], :, t % page // 16], t % 16
+            gr[:, 8 * D + r * (D // 16):8 * D + (r + 1) * (D // 16)] = 0x7F
+            gr[:, r * (D // 2):(r + 1) * (D // 2)] = 0xA5
+            gr[:, 17 * D + r::16] = 0xFF
+    o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs, window=window)
+    assert st == 0 and torch.equal(o, want)
