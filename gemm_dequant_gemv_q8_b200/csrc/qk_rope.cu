@@ -103,11 +103,13 @@ __device__ __forceinline__ void load_turn(const float* row, int rot, int d0, flo
 }
 
 // Norm (where `norm` says so) and rotation (of the lanes that `turn`) of one head in the arithmetic of R: float, or
-// double for keys that are quantized.  Every lane of the D / 8 lanes of a head calls it.
+// double for keys that are quantized.  Every lane of the D / 8 lanes of a head calls it.  False for all of them where the
+// squares leave the range of R.
 template <typename R, int D, int TURN>
-__device__ __forceinline__ void norm_rope(float (&v)[8], bool norm, const float (&w)[8], float eps, bool turn, int rot, int d0,
+__device__ __forceinline__ bool norm_rope(float (&v)[8], bool norm, const float (&w)[8], float eps, bool turn, int rot, int d0,
                                           const float (&c)[8], const float (&s)[8]) {
     R n[8];
+    bool in_range = true;
 #pragma unroll
     for (int j = 0; j < 8; ++j) n[j] = (R)v[j];
     if (norm) {
@@ -118,10 +120,12 @@ __device__ __forceinline__ void norm_rope(float (&v)[8], bool norm, const float 
         for (int m = D / 16; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
         const R ms = ss * (R)(1.0 / D) + (R)eps;
         R r;
-        if constexpr (sizeof(R) == 8)
+        if constexpr (sizeof(R) == 8) {
             r = rsqrt(ms);
-        else
+        } else {
             r = rsqrtf(ms);  // within 2 ulp
+            in_range = ms >= 0x1p-100f && ms <= 0x1p126f;
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) n[j] = n[j] * r * (R)w[j];
     }
@@ -145,6 +149,11 @@ __device__ __forceinline__ void norm_rope(float (&v)[8], bool norm, const float 
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = (float)n[j];
+    return in_range;
+}
+
+__device__ __forceinline__ float amax4(const float* v) {
+    return fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 }
 
 // The scale byte of a block whose largest magnitude is m, under scale g: E4M3(m / (6 g)).  div_by_recip gives the correctly
@@ -174,9 +183,6 @@ __device__ __forceinline__ void block_codes(const float* v, float m, uint8_t s, 
         for (int j = 0; j < 2 * N; ++j)
             codes[j / 2] |= e2m1x2_rne_sat(__fdiv_rn(v[2 * j], div), __fdiv_rn(v[2 * j + 1], div)) << (8 * (j & 1));
     }
-}
-__device__ __forceinline__ float amax4(const float* v) {
-    return fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 }
 
 // APPEND: heads are [q | k | v]; q to bf16 rows, k and v to the cache.  Otherwise [q | k] to rows of Y.
@@ -232,15 +238,46 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs
     if (turn) load_turn<TURN>(a.cs + pos * a.rot, a.rot, d0, cs, sn);
     if (!APPEND || kind == 0) {
         Y* out = kind == 0 ? reinterpret_cast<Y*>(a.q) + t * a.ldq : reinterpret_cast<Y*>(a.k) + t * a.ldk;
+        unsigned again = 0;  // heads whose squares leave the range of 32 bits
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float v[8];
             raw[i].get(v);
-            norm_rope<float, D, TURN>(v, norm, w, a.eps, turn, a.rot, d0, cs, sn);
+            const bool good = norm_rope<float, D, TURN>(v, norm, w, a.eps, turn, a.rot, d0, cs, sn);
             if (h0 + i * HPW < heads) {
-                Y* dst = out + (int64_t)(h0 + i * HPW) * D;
-                store4(dst + d0, v);
-                store4(dst + d1, v + 4);
+                if (good) {
+                    Y* dst = out + (int64_t)(h0 + i * HPW) * D;
+                    store4(dst + d0, v);
+                    store4(dst + d1, v + 4);
+                } else {
+                    again |= 1u << i;
+                }
+            }
+        }
+        // Those once more, from memory (they have not been written, also where q and k are x's own heads): the head, and the
+        // root of eps, times a power of two that brings the squares into the range; the norm is the same.
+        if (__any_sync(0xffffffffu, again != 0)) {
+#pragma unroll 1
+            for (int i = 0; i < N; ++i) {
+                const bool mine = (again >> i) & 1;
+                Raw8<X> one;
+                if (mine)
+                    one.load(row + (int64_t)(h0 + i * HPW) * D, d0, d1);
+                else
+                    one.zero();
+                float v[8];
+                one.get(v);
+                const bool large = fmaxf(fmaxf(amax4(v), amax4(v + 4)), a.eps) >= 1.f;
+                const unsigned larges = __ballot_sync(0xffffffffu, large) >> (sub * LPH) & ((1u << LPH) - 1);
+                const float s = larges ? 0x1p-70f : 0x1p90f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] *= s;
+                norm_rope<float, D, TURN>(v, norm, w, a.eps * s * s, turn, a.rot, d0, cs, sn);
+                if (mine) {
+                    Y* dst = out + (int64_t)(h0 + i * HPW) * D;
+                    store4(dst + d0, v);
+                    store4(dst + d1, v + 4);
+                }
             }
         }
     } else {

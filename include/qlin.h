@@ -438,10 +438,8 @@ typedef struct qlin_qk_params {
  *       ldx elements, 16-byte aligned rows (ldx a multiple of 4 (fp32) or 8 (bf16))
  *   positions : T int32, the tokens' rows of cos_sin; not read where rot is 0
  *   q, k : T rows of Hq * D and Hkv * D values, fp32 or bf16 (ydt), row strides ldq and ldk elements,
- *       rows aligned as x's; the arithmetic is fp32, rounded once (where the sum of a
- *       head's squares overflows, for values of 2^60 and more, its norm gives zeros).  q and k may
- *       overwrite x's own heads (q = x, k = x + Hq * D, the same strides and type), and nothing else
- *       of x.
+ *       rows aligned as x's; the arithmetic is fp32, rounded once.  q and k may overwrite x's own heads
+ *       (q = x, k = x + Hq * D, the same strides and type), and nothing else of x.
  *   ws : 256 bytes (the status word), zero-filled before first use
  * T = 0 does nothing.  A position outside [0, n_pos) leaves its token's q and k rows unwritten and
  * sets the status word (qlin_ws_status: QLIN_ERR_INVALID_ARG). */

@@ -166,3 +166,32 @@ def test_attention_uses_nothing_before_the_window(nq, window):
             gr[:, 17 * D + r::16] = 0xFF
     o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs, window=window)
     assert st == 0 and torch.equal(o, want)
+
+
+RANGE = [(F32, 0.0, 2.0 ** 62), (F32, 1e-6, 2.0 ** 100), (F32, 1e-6, 2.0 ** 126), (F32, 0.0, 2.0 ** -70), (F32, 0.0, 2.0 ** -130),
+         (BF16, 0.0, 2.0 ** 64), (BF16, 0.0, 2.0 ** -80), (F32, 1e-38, 2.0 ** -64), (F32, 1e38, 2.0 ** 63), (F32, 3e38, 1.0)]
+
+
+@pytest.mark.parametrize("xdt,eps,size", RANGE)
+@pytest.mark.parametrize("D,rot,inter", [(128, 128, False), (64, 32, True), (128, 16, False)])
+def test_norms_over_the_whole_range(xdt, eps, size, D, rot, inter):
+    T, Hq, Hkv = 7, 5, 2
+    g = gen(4)
+    x = torch.randn(T, (Hq + Hkv) * D, generator=g)
+    x[:, :3 * D] *= size / 4
+    x[:, (Hq + 1) * D:] *= size / 4
+    x = x.to(xdt)
+    assert torch.isfinite(x).all()
+    w = [1 + 0.3 * torch.randn(D, generator=g) for _ in range(2)]
+    pos, cs = torch.arange(T, dtype=torch.int32), ref.table(T, rot)
+    qo, ko = q.qlin_qk_norm_rope(x.cuda(), Hq, Hkv, D, pos.cuda(), cs.cuda(), w[0].cuda(), w[1].cuda(), eps, flags=int(inter), ydt=q.QLIN_F32)
+    xd = x.double().view(T, Hq + Hkv, D)
+    for got, part, wt in ((qo, xd[:, :Hq], w[0]), (ko, xd[:, Hq:], w[1])):
+        y, A = ref.norm_rope(part, wt, eps, cs, pos, rot, inter)
+        assert ((got.cpu().double() - y).abs() <= rope_tol(y, A, F32)).all()
+    # in place: heads that are written late are read first
+    xc, dt = x.cuda(), q.QLIN_F32 if xdt == F32 else q.QLIN_BF16
+    args = (Hq, Hkv, D, pos.cuda(), cs.cuda(), w[0].cuda(), w[1].cuda(), eps)
+    want = torch.cat([t.flatten(1) for t in q.qlin_qk_norm_rope(xc, *args, flags=int(inter), ydt=dt)], 1)
+    q.qlin_qk_norm_rope(xc, *args, flags=int(inter), ydt=dt, q=xc[:, :Hq * D], k=xc[:, Hq * D:])
+    assert torch.equal(xc, want)
