@@ -37,13 +37,19 @@ def _stale():
 
 
 def build_binding(force: bool = False) -> str:
-    """The argument marshalling of the cache's and the attention's calls (csrc/torch_binding.cpp)."""
-    deps = [BINDING_SRC, os.path.join(ROOT, "include", "qlin.h")]
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
-        return BINDING
+    """The argument marshalling of the cache's and the attention's calls (csrc/torch_binding.cpp), for the installed torch
+    and Python."""
     import sysconfig
 
     import torch
+    made_for = f"torch {torch.__version__}, python {sys.version.split()[0]}, abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}\n"
+    stamp = os.path.join(HERE, "_build", "_qlin_torch.for")
+    deps = [BINDING_SRC, os.path.join(ROOT, "include", "qlin.h")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
+        if os.path.exists(stamp):
+            with open(stamp) as f:
+                if f.read() == made_for:
+                    return BINDING
     here = os.path.dirname(torch.__file__)
     includes = [os.path.join(here, "include"), os.path.join(here, "include", "torch", "csrc", "api", "include"),
                 os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), sysconfig.get_paths()["include"]]
@@ -53,11 +59,20 @@ def build_binding(force: bool = False) -> str:
                            *(a for p in includes for a in ("-isystem", p)), BINDING_SRC, "-o", tmp,
                            "-L", os.path.join(here, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
     os.replace(tmp, BINDING)
+    os.makedirs(os.path.dirname(stamp), exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(made_for)
     return BINDING
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """The library, which needs nvcc alone, then the binding; returns the library's path."""
+    build_library(force, verbose)
     build_binding(force)
+    return LIB
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     objs = []
