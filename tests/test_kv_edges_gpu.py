@@ -7,7 +7,7 @@ import torch
 
 import gemm_dequant_gemv_q8_b200 as q
 import kv_reference as ref
-from test_kv_attn_gpu import BF16, F32, attn_case, gen, rope_tol, run_attn
+from test_kv_attn_gpu import BF16, F32, attn_case, check_attn, gen, rope_tol, run_attn
 
 pytestmark = pytest.mark.gpu
 
@@ -195,3 +195,86 @@ def test_norms_over_the_whole_range(xdt, eps, size, D, rot, inter):
     want = torch.cat([t.flatten(1) for t in q.qlin_qk_norm_rope(xc, *args, flags=int(inter), ydt=dt)], 1)
     q.qlin_qk_norm_rope(xc, *args, flags=int(inter), ydt=dt, q=xc[:, :Hq * D], k=xc[:, Hq * D:])
     assert torch.equal(xc, want)
+
+
+def masked_attention(qs, k, v, L, scale, valid, window=0):
+    """ref.attention with a mask of a sequence's places beside the causal one, a row at a time: (out, tol)."""
+    n, Hq, D = qs.shape
+    G = Hq // k.shape[1]
+    out, tol = torch.zeros(n, Hq, D, dtype=torch.float64), torch.zeros(n, Hq, D, dtype=torch.float64)
+    for i in range(n):
+        p = L - n + i
+        idx = torch.arange(max(0, p - window + 1) if window else 0, p + 1)
+        idx = idx[valid[idx]]
+        if len(idx) == 0:
+            continue
+        o, tp, ts, tv = ref.attention(qs[i:i + 1].double(), k[idx], v[idx], len(idx), scale)
+        out[i], tol[i] = o[0], ref.attention_tol(o, tp, ts, tv, D, len(idx))[0]
+    return out, tol
+
+
+@pytest.mark.parametrize("nq,window", [(1, 0), (5, 0), (40, 0), (300, 0), (40, 200), (5, 90)])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 128)])
+def test_attention_missing_pages_are_masked_places(nq, window, D, page):
+    # Pages outside the cache in many tiles of a long context, in the first ones of another, and all of a third's: rows that
+    # see nothing are zeros.
+    lens, Hq, Hkv = [1900, 700, 310], 8, 2
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, [nq] * 3, Hq, Hkv, D, page, 110)
+    valid = [torch.ones(L, dtype=torch.bool) for L in lens]
+
+    def drop(b, j, number):
+        table[b, j] = number
+        valid[b][j * page:(j + 1) * page] = False
+
+    for j in range(0, -(-lens[0] // page), 3):
+        drop(0, j, 10 ** 6 if j % 2 else -1 - j)
+    for j in range(max(1, -(-(lens[1] - nq // 2) // page))):
+        drop(1, j, len(c) // q.qlin_kv_cache_bytes(1, page, Hkv, D))  # the first number behind the cache
+    for j in range(-(-lens[2] // page)):
+        drop(2, j, -2 ** 31)
+    o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs, window=window)
+    assert st == 1
+    o = o.cpu().double()
+    for b, L in enumerate(lens):
+        want, tol = masked_attention(qs[b], ks[b], vs[b], L, D ** -0.5, valid[b], window)
+        got = o[cu[b]:cu[b + 1]]
+        assert ((got - want).abs() <= tol).all(), (b, float(((got - want).abs() - tol).max()))
+
+
+@pytest.mark.parametrize("nq", [1, 3, 16, 64, 300])
+@pytest.mark.parametrize("L,Hq,Hkv,D,page,window", [(30000, 8, 4, 64, 64, 0), (100001, 4, 4, 128, 16, 0), (5001, 32, 2, 64, 128, 0),
+                                                    (40000, 8, 1, 128, 256, 17777), (1000, 24, 8, 64, 32, 0)])
+def test_every_token_counts_once(nq, L, Hq, Hkv, D, page, window):
+    # All scores are 0, so every seen token has the same weight, and the tokens of group i (16 tokens) have the value 6 at
+    # place i % D: an output value is 6 times the share of the tokens whose value it is.  The sums are exact (whole multiples of
+    # one power of two, below 2^24 of them); the quotient, the product with it and the output are rounded (2^-24 each for the
+    # first two, at most 2^-8).
+    t = torch.arange(L, device="cuda")
+    v = torch.zeros(L, Hkv, D, device="cuda")
+    v[t, :, t // 16 % D] = 6
+    cache = exact_cache(torch.zeros(L, Hkv, D, device="cuda"), v, page)
+    o = call(cache, L, nq, Hq, window=window).double()
+    counts = torch.zeros(L + 1, D, dtype=torch.float64, device="cuda")
+    counts[1:] = (v[:, 0] / 6).double().cumsum(0)
+    p = torch.arange(L - nq, L, device="cuda")
+    first = (p - window + 1).clamp(min=0) if window else torch.zeros_like(p)
+    want = 6 * (counts[p + 1] - counts[first]) / (p + 1 - first)[:, None]
+    err = (o - want[:, None]).abs()
+    assert (err <= (2.0 ** -8 + 4 * 2.0 ** -24) * want[:, None]).all(), float((err / want[:, None]).max())
+
+
+MIXED = [  # queries, contexts, Hq, Hkv, D, page, window
+    ([1] * 12 + [300, 1, 0, 1], [77 * (b + 1) for b in range(12)] + [900, 64, 5, 4000], 8, 2, 128, 64, 0),
+    ([1, 1, 8, 1, 0, 2], [500, 3, 2000, 128, 40, 33], 8, 1, 64, 16, 0),       # few rows: one and eight row blocks' worth
+    ([130, 1, 1, 130], [130, 2500, 1, 131], 4, 4, 64, 32, 100),
+    ([1, 32, 1], [6000, 32, 700], 32, 8, 128, 16, 0),
+]
+
+
+@pytest.mark.parametrize("nqs,lens,Hq,Hkv,D,page,window", MIXED)
+def test_single_tokens_beside_chunks(nqs, lens, Hq, Hkv, D, page, window):
+    # every sequence of a call as it is alone
+    c, table, ln, cu, qs, ks, vs = attn_case(lens, nqs, Hq, Hkv, D, page, 120)
+    o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs, window=window)
+    assert st == 0
+    check_attn(o, ln, cu, qs, ks, vs, D, D ** -0.5, window)
