@@ -17,13 +17,15 @@
 // The exponents' reference follows the running maximum only when that has grown by 2^8 (kBelow, kGrow), so O is rarely
 // rescaled.
 //
-// 2 x 2047 queries of 8189 tokens (32 heads of 128): 381 us, 863 TFLOP/s; 8192 of 8192: 608 us, 905 TFLOP/s.  The bound is
-// the chain of a tile of rows: 1.55 us of softmax, then 0.8 us until its next scores are there, while the tensor cores
-// have 1.1 us of work and the special function units as much for both tiles; two tiles (scores and O: 512 columns) fill
-// tensor memory.  Two threads a row (493 us), scores in halves of 64 (485) and exponentials by polynomial for a part of
-// the scores (384 to 410) were slower: issue slots are as scarce as the special function unit.
-// Units are dealt out heaviest first, there and back; those of the last, partial round are split along the tokens
-// where that shortens it, and the last CTA of a unit to finish joins its parts in their order.
+// 2 x 2047 queries of 8189 tokens (32 heads of 128): 371 us, 886 TFLOP/s; 8192 of 8192: 594 us, 926 TFLOP/s.  The bound is
+// the chain of a tile of rows: 1.55 us of softmax, then 0.8 us until its next scores are there (measured at 381 us),
+// while the tensor cores have 1.1 us of work and the special function units as much for both tiles; two tiles (scores
+// and O: 512 columns) fill tensor memory.  No unit is full (issue 48%, special functions 43%, tensor cores 43% of the
+// cycles).  Two threads a row (493 us), scores in halves of 64 (485) and exponentials by polynomial for a part of the
+// scores (384 to 410) were slower than 381.
+// Units are dealt out there and back, sequences as they stand and in each the heaviest first (a long prompt behind a short
+// one costs: 512 of 512, then 2047 of 8189 346 us, the other way round 283); those of the last, partial round are split
+// along the tokens where that shortens it, and the last CTA of a unit to finish joins its parts in their order.
 // Every wait is bounded; a timeout sets the status word and the CTA winds down.
 #include <cuda/std/type_traits>
 

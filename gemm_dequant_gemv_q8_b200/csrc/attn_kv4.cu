@@ -25,10 +25,13 @@ namespace kv {
 // operands share it: for S it is the order in which a lane's 16 (8) bytes of a token's row hold the values, for P V the
 // lanes' tokens are four neighbours, whose codes of one block are 32 contiguous bytes.
 //
-// The cache has to be read once, and is; what bounds the kernel is the arithmetic that dequantizes it (one conversion a
-// byte and one product a pair of values: ALU pipe 50% busy, an instruction issued in 56% of the active cycles) beside
-// some 9 us of start and end (launch, lengths and pages, the joining).  64 sequences of up to 8192 tokens (8 kv heads of
-// 128, 374 MB): 104 us, 3.6 TB/s; the copies alone 67, without V's arithmetic 80, without K's 89.  1 x 131071 40 us
+// The cache has to be read once, and is for single tokens; a call's largest sequence gives the row blocks of all, and each
+// reads the context, also one without rows (32 x 2000 tokens, single tokens 32 us; with one sequence of 8 queries of four
+// heads 69).  No pipe is full (ALU 50%, tensor cores 23%, HBM 42%, an instruction issued in 56% of the active cycles): the
+// kernel is bound by the dequantizing arithmetic's instructions and their latencies together (one conversion a byte and one
+// product a pair of values), beside some 9 us of start and end (launch, lengths and pages, the joining).  64 sequences of
+// up to 8192 tokens (8 kv heads of 128, 374 MB): 104 us, 3.6 TB/s; the copies alone 67, without V's arithmetic 80,
+// without K's 89.  1 x 131071 40 us
 // (3.8 TB/s); 16 x 4096 ragged (heads of 64, 24 MB) 20; 1 x 1000 9.5.  Warps: 16 give 102 / 41 / 20.1 us on the first
 // three (before the shares), 12 105 / 44 / 20.8, 8 114 / 47 / 21.1.
 template <int D, int NT>
@@ -723,7 +726,8 @@ static int kv_sm_count() {
 // Whether the kernel for few rows takes a call.  It goes over the cache once for every 16 query rows of a kv head, but
 // spreads any context over all SMs; the one for chunks goes over it once for 256, in units of at least 128 rows.  us, few
 // rows against chunks: 1 x 8000 tokens (8 kv heads) 64 rows 28 / 47, 128 rows 38 / 49; 8 x 2000 32 rows 27 / 34, 64 rows
-// 41 / 34; 32 x 4000 32 rows 117 / 167, 64 rows 216 / 168.
+// 41 / 34; 32 x 4000 32 rows 117 / 167, 64 rows 216 / 168.  max_q decides for the whole call: single tokens beside a prompt
+// chunk go the chunks' way (31 of 4000 and a chunk of 512 153 us; in two calls 44 and 20).
 static bool few_rows(int64_t rows, int B, int Hkv) {
     return rows <= 32 || (rows <= 128 && rows * B * Hkv <= 2048);
 }

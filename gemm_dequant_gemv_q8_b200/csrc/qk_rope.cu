@@ -16,8 +16,8 @@ namespace qlin {
 namespace kv {
 
 // Heads a warp.  What is only normed and rotated: 8, so that a token's row of the table and the weights are loaded once for
-// many (2048 tokens: 8.5 us, 9.8 with 4).  What is quantized: 4, for the path is long and its code repeated for each
-// (8192 tokens appended: 54 us, 73 with 8).
+// many (2048 tokens: 8.6 us, 9.8 with 4).  What is quantized: 4, for the path is long and its code repeated for each
+// (8192 tokens appended: 53 us, 73 with 8).
 constexpr int kHeadsPerWarp = 8;
 constexpr int kQuantHeadsPerWarp = 4;
 constexpr int kRopeWarps = 2;

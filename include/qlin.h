@@ -497,8 +497,9 @@ size_t qlin_attn_kv4_workspace_bytes(const qlin_kv_cache* cache, int B, int max_
  *       context, before the window) are not looked at
  *   seq_lens : B int32; cu_q : B + 1 int32, not falling; both device arrays, so one captured graph serves any lengths
  *   scale : finite, and 2 * scale * k_scale too
- *   max_q : the most queries of one sequence in this call (it chooses the kernel and sizes ws); Hq a multiple of Hkv,
- *       Hq / Hkv <= 64; B <= 1024
+ *   max_q : the most queries of one sequence in this call (it chooses the kernel, for all sequences, and sizes ws: single
+ *       tokens are faster in a call of their own than beside longer sequences); Hq a multiple of Hkv, Hq / Hkv <= 64;
+ *       B <= 1024
  *   ws : qlin_attn_kv4_workspace_bytes(cache, B, max_q, Hq) bytes, zero-filled before first use; it may
  *       be reused by any later qlin_attn_kv4 call on the same stream for which it is large enough
  * A sequence with n outside [0, max_q], rows outside [0, total_q) or L outside [0, max_pages * page] is
