@@ -1,5 +1,5 @@
 """Edges of the cache's and the attention's calls: far tails of a softmax, scores near the limits of 32 bits, NaN and
-junk in the cache, the range of the norms, pages that are missing, every token counted once."""
+junk in the cache, the range of the norms, pages that are missing, every token counted once, mixed batches, the largest sizes."""
 import math
 
 import pytest
@@ -278,3 +278,50 @@ def test_single_tokens_beside_chunks(nqs, lens, Hq, Hkv, D, page, window):
     o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs, window=window)
     assert st == 0
     check_attn(o, ln, cu, qs, ks, vs, D, D ** -0.5, window)
+
+
+@pytest.mark.parametrize("nq,Hq,Hkv", [(1, 4, 1), (5, 8, 2), (200, 2, 1)])
+@pytest.mark.parametrize("L", [2 ** 26, 2 ** 26 - 37])
+def test_the_longest_context(nq, Hq, Hkv, L):
+    # 2^26 tokens through a table that names eight pages again and again.  As above, but the sums of so many tokens are rounded:
+    # each warp or part sums up to some 2^20 equal terms (below 2^24 of them: exact), then 2^12 at most are joined (2^-24 each).
+    D, page, P = 64, 256, 8
+    v = torch.zeros(P * page, Hkv, D, device="cuda")
+    t = torch.arange(P * page, device="cuda")
+    v[t, :, t // 16 % D] = 6
+    cache = exact_cache(torch.zeros_like(v), v, page)
+    n = -(-L // page)
+    table = torch.randint(0, P, (n,), generator=gen(5), dtype=torch.int32)
+    ws = q.workspace(q.qlin_attn_kv4_workspace_bytes(cache, 1, nq, Hq))
+    o = q.qlin_attn_kv4(cache, torch.zeros(nq, Hq, D, dtype=BF16, device="cuda"), table[None].cuda(),
+                        torch.tensor([L], dtype=torch.int32).cuda(), torch.tensor([0, nq], dtype=torch.int32).cuda(), nq, ws=ws)
+    assert q.qlin_ws_status(ws) == 0
+    o = o.double().cpu()
+    ones = (v[:, 0].view(P, page, D) / 6).double().cpu()
+    counts = torch.bincount(table[:n - 1].long(), minlength=P).double() @ ones.sum(1)
+    for i in range(nq):
+        seen = L - nq + i + 1
+        want = 6 * (counts + ones[int(table[-1])][:seen - (n - 1) * page].sum(0)) / seen
+        assert seen > (n - 1) * page and ((o[i] - want).abs() <= (2.0 ** -8 + 2.0 ** -12) * want).all()
+
+
+def test_the_longest_chunk():
+    # 2^20 queries over their own tokens: query i averages the first i + 1
+    n, D, page = 1 << 20, 64, 256
+    v = torch.zeros(n, 1, D, device="cuda")
+    t = torch.arange(n, device="cuda")
+    v[t, :, t // 16 % D] = 6
+    cache = exact_cache(torch.zeros_like(v), v, page)
+    o = call(cache, n, n, 1)[:, 0].double()
+    want = 6 * (v[:, 0] / 6).double().cumsum(0) / (t + 1)[:, None]
+    assert ((o - want).abs() <= (2.0 ** -8 + 2.0 ** -12) * want).all()
+
+
+@pytest.mark.parametrize("nq", [1, 3, 40])
+@pytest.mark.parametrize("G", [1, 2])
+def test_the_most_heads(nq, G):
+    Hq, Hkv, D, page = 1024, 1024 // G, 64, 16
+    c, table, ln, cu, qs, ks, vs = attn_case([100, 37], [nq] * 2, Hq, Hkv, D, page, 130)
+    o, st = run_attn(c, page, Hkv, D, table, ln, cu, qs)
+    assert st == 0
+    check_attn(o, ln, cu, qs, ks, vs, D, D ** -0.5)
